@@ -356,6 +356,146 @@ fp8_status fp8_quantize_static_scratch(const fp8_recipe *recipe, const void *x_b
                                        int32_t want_row, int32_t want_col, fp8_tensor *out,
                                        int32_t *dev_status, cudaStream_t stream);
 
+/*
+ * RMSNorm in front of the FP8 linear layer. The norm reads the residual stream, and its output
+ * is the linear layer's X, so it writes X's FP8 copies itself instead of a bf16 tensor that
+ * fp8_quantize would read back.
+ *
+ *   h = bf16(x + residual)            (h = x when there is no residual)
+ *   rstd[r] = 1 / sqrt(mean_c h[r][c]^2 + eps)                          fp32
+ *   y[r][c] = (h[r][c] * rstd[r]) * gamma[c]                            fp32, two roundings
+ *
+ * The residual stream is held in bf16, and the norm is taken of the stream as stored, so the
+ * backward pass, which reads h, differentiates the function that ran. y is quantised straight
+ * from fp32 (no bf16 rounding in between) by the rules above.
+ */
+
+/* Inputs of the norm, device pointers, 16-byte aligned. Row pitches in elements, multiples of
+ * 8, >= cols. */
+typedef struct {
+  const void *x;         /* [rows][cols] bf16, row pitch ldx */
+  const void *residual;  /* [rows][cols] bf16, row pitch ldr, or NULL */
+  const void *gamma;     /* [cols] bf16 (gamma_fp32 = 0) or fp32 (1) */
+  int64_t ldx, ldr;
+  int64_t rows, cols;
+  int32_t gamma_fp32;
+  float eps;             /* >= 0 and finite; with eps 0 a row of zeros gives NaN (0 * inf) */
+} fp8_norm_input;
+
+/* Bytes of scratch fp8_rmsnorm_quantize needs (0 for a NULL recipe: the bf16 output alone). */
+size_t fp8_rmsnorm_workspace_bytes(const fp8_recipe *recipe, int64_t rows, int64_t cols);
+
+/*
+ * fp8_rmsnorm_quantize — residual addition, RMSNorm and the FP8 copies of its output.
+ *   recipe     as for fp8_quantize (role ACTIVATION: E4M3 codes; with --fp8-wgrad off the
+ *              column copy is the bf16 transpose of bf16(y)). May be NULL when neither copy is
+ *              wanted: then only y_bf16 (and h, rstd) are written.
+ *   in         the inputs. rows is any number >= 0 (a single token when serving); cols is a
+ *              multiple of 16, and of 128 for MXFP8 and BLOCKWISE, at most 32768.
+ *   h_bf16     [rows][cols] bf16, contiguous: the new residual stream. Required with a
+ *              residual, not written (may be NULL) without. May be in->x or in->residual
+ *              itself when that is contiguous (an update in place).
+ *   rstd       [rows] fp32 for the backward pass, or NULL.
+ *   y_bf16     [rows][cols] bf16(y), contiguous, or NULL.
+ *   want_row / want_col: which copies to write into `out`.
+ *   out        the copies of y padded with rows of zeros to a multiple of the recipe's row
+ *              quantum q (128 for MXFP8 and BLOCKWISE, 16 otherwise): out->rows is that padded
+ *              count, the buffers hold it, and the padding's codes and scales are those of
+ *              zeros, so a GEMM of the padded tensor can follow. A padded size of 2^31 elements or more is
+ *              refused. DELAYED reads out->scale and writes out->amax (fp8_amax_update follows);
+ *              TENSORWISE writes amax, scale and scale_inv.
+ *   workspace  fp8_rmsnorm_workspace_bytes() of device scratch.
+ * NaN in y gives code 0x7F; an Inf or NaN anywhere in a row reaches the whole row. Apart from h
+ * no output may overlap an input. Source: the norm in front of each linear layer of the
+ * transformer block that the "Low-Precision Training Guide" trains (section "When to Use Low
+ * Precision"); the formulas and the fusion are this library's.
+ */
+fp8_status fp8_rmsnorm_quantize(const fp8_recipe *recipe, const fp8_norm_input *in,
+                                int32_t want_row, int32_t want_col, void *h_bf16, float *rstd,
+                                void *y_bf16, fp8_tensor *out, void *workspace, size_t ws_bytes,
+                                int32_t *dev_status, cudaStream_t stream);
+
+/* Inputs of the norm's backward pass; pointers and pitches as for fp8_norm_input. */
+typedef struct {
+  const void *dy;        /* [rows][cols] bf16: the gradient of y (fp8_linear_bwd's dx), pitch ld_dy */
+  const void *h;         /* [rows][cols] bf16: the stream the norm read, pitch ld_h */
+  const void *dres;      /* [rows][cols] bf16: the gradient of h on the residual path, pitch
+                            ld_dres, or NULL */
+  const void *gamma;     /* [cols] */
+  const float *rstd;     /* [rows], as the forward pass wrote it */
+  int64_t ld_dy, ld_h, ld_dres;
+  int64_t rows, cols;
+  int32_t gamma_fp32;
+} fp8_norm_grad;
+
+/* Bytes of scratch fp8_rmsnorm_bwd needs (0 when dgamma is not wanted). */
+size_t fp8_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * fp8_rmsnorm_bwd — backward of the norm and of the residual addition.
+ *   xh = h * rstd,  t = dy * gamma,  c[r] = mean_c(t * xh)
+ *   dh = bf16(dres + rstd * (t - xh * c))      the gradient of x and of residual alike
+ *   dgamma[c] = sum_r dy * xh                  fp32, a fixed order of additions
+ *   dh_bf16    [rows][cols] bf16, contiguous; may be in->dy or in->dres itself when that is
+ *              contiguous.
+ *   dgamma     [cols] fp32, 16-byte aligned, overwritten (zeros when rows is 0), or NULL.
+ *   workspace  fp8_rmsnorm_bwd_workspace_bytes() of device scratch (NULL without dgamma).
+ * rows >= 0; cols a multiple of 16, at most 32768.
+ */
+fp8_status fp8_rmsnorm_bwd(const fp8_norm_grad *in, void *dh_bf16, float *dgamma, void *workspace,
+                           size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/*
+ * The gradients of a step, before the optimizer: their global norm and clipping by it.
+ *   norm = scale * sqrt(sum over all tensors of g^2)
+ *   coef = scale * min(1, max_norm / (norm + 1e-6))
+ *   out  = g * coef
+ */
+
+/* Element types of a gradient. */
+typedef enum { FP8_GRAD_BF16 = 0, FP8_GRAD_FP32 = 1 } fp8_grad_dtype;
+
+/* One gradient tensor: `numel` elements, dense, in any order. Pointers are aligned to their
+ * element only (views into a packed buffer). `out` is read by fp8_grad_clip alone; it may be
+ * `grad` itself (in place, same type) and must not overlap any gradient otherwise. */
+typedef struct {
+  const void *grad;
+  void *out;
+  int64_t numel;         /* >= 0 */
+  int32_t dtype;         /* fp8_grad_dtype of grad */
+  int32_t out_dtype;     /* fp8_grad_dtype of out */
+} fp8_grad_item;
+
+typedef struct {
+  float max_norm;        /* > 0; infinity: no clipping (coef = scale) */
+  float scale;           /* > 0, finite: the factor each gradient stands for (one over the
+                            number of micro batches, or over a loss scale); 1 for none */
+} fp8_clip_rule;
+
+/* Bytes of scratch fp8_grad_norm needs for n tensors. */
+size_t fp8_grad_workspace_bytes(int32_t n);
+
+/*
+ * fp8_grad_norm — the global norm of n gradients and the clip coefficient that follows from it.
+ *   items      n descriptions in host memory, read during the call only (n >= 0).
+ *   norm, coef device fp32 scalars; coef may be NULL.
+ *   workspace  fp8_grad_workspace_bytes(n) of device scratch.
+ * Squares are added in fp32 in a fixed order, so equal inputs give equal bits, and the sums of
+ * blocks in fp64; values whose squares leave fp32's range are squared in fp64. An infinite or
+ * NaN gradient makes the norm infinite or NaN, and coef 0 or NaN: the caller looks at the norm.
+ */
+fp8_status fp8_grad_norm(int32_t n, const fp8_grad_item *items, const fp8_clip_rule *rule,
+                         float *norm, float *coef, void *workspace, size_t ws_bytes,
+                         cudaStream_t stream);
+
+/*
+ * fp8_grad_clip — out = g * *coef for n gradients, rounded once to out's type. coef is a device
+ * scalar, as fp8_grad_norm writes it. A coef of 1 leaves tensors that are clipped in place
+ * untouched.
+ */
+fp8_status fp8_grad_clip(int32_t n, const fp8_grad_item *items, const float *coef,
+                         cudaStream_t stream);
+
 /* Human-readable name of a status. */
 const char *fp8_status_str(fp8_status status);
 

@@ -524,3 +524,59 @@ def dgelu_bf16(da_bf16, h_codes, h_e8m0):
     """dh = bf16(da * gelu'(deq(h_fp8))): the backward reads h back from its FP8 copy."""
     h = dequant_mx(h_codes, h_e8m0)
     return f64_to_bf16(bf16_to_f32(da_bf16).astype(np.float64) * gelu_grad_f64(h))
+
+
+# --------------------------------------------------------------------------------------
+# RMSNorm around the linear layer, gradient norm and clipping
+# --------------------------------------------------------------------------------------
+
+def residual_add_bf16(x_bf16, res_bf16):
+    """h = bf16(x + residual): the sum in float64 (exact for two bf16 values whose exponents are
+    less than 45 apart, and the larger one's own rounding beyond), rounded once."""
+    return f64_to_bf16(bf16_to_f32(x_bf16).astype(np.float64)
+                       + bf16_to_f32(res_bf16).astype(np.float64))
+
+
+def rmsnorm_rstd_f64(h, eps):
+    """1 / sqrt(mean over a row of h^2 + eps), float64 [rows]."""
+    h = np.asarray(h, dtype=np.float64)
+    return 1.0 / np.sqrt(np.mean(h * h, axis=1) + float(eps))
+
+
+def rmsnorm_f64(h, gamma, eps):
+    """y = h / sqrt(mean h^2 + eps) * gamma, float64."""
+    h = np.asarray(h, dtype=np.float64)
+    return h * rmsnorm_rstd_f64(h, eps)[:, None] * np.asarray(gamma, dtype=np.float64)
+
+
+def rmsnorm_y_f32(h_bf16, rstd_f32, gamma_f32):
+    """The value that is quantised: (h * rstd) * gamma, each product rounded to float32."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        t = bf16_to_f32(h_bf16) * np.asarray(rstd_f32, dtype=np.float32)[:, None]
+        return t * np.asarray(gamma_f32, dtype=np.float32)
+
+
+def rmsnorm_bwd_f64(dy, h, rstd, gamma, dres=None):
+    """(dh, dgamma) of y = h rstd(h) gamma for a gradient dy of y, float64:
+    dh = dres + rstd (t - xh mean(t xh)) with xh = h rstd, t = dy gamma; dgamma = sum dy xh."""
+    dy, h = np.asarray(dy, dtype=np.float64), np.asarray(h, dtype=np.float64)
+    r = np.asarray(rstd, dtype=np.float64)[:, None]
+    xh, t = h * r, dy * np.asarray(gamma, dtype=np.float64)
+    dh = r * (t - xh * np.mean(t * xh, axis=1, keepdims=True))
+    if dres is not None:
+        dh = dh + np.asarray(dres, dtype=np.float64)
+    return dh, np.sum(dy * xh, axis=0)
+
+
+def grad_norm_f64(grads, scale=1.0):
+    """scale * the square root of the sum over all tensors of their squares, float64."""
+    return float(scale) * math.sqrt(sum(float(np.sum(np.square(np.asarray(g, dtype=np.float64))))
+                                        for g in grads))
+
+
+def clip_coef_f64(norm, max_norm, scale=1.0):
+    """scale * min(1, max_norm / (norm + 1e-6)); NaN stays NaN, an infinite norm gives 0."""
+    if math.isinf(max_norm):
+        return float(scale)
+    c = max_norm / (norm + 1e-6)
+    return float(scale) * (1.0 if c > 1.0 else c)

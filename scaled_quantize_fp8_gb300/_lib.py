@@ -50,6 +50,33 @@ class AmaxHistory(ctypes.Structure):
     _fields_ = [("history", ctypes.c_void_p), ("head", ctypes.c_void_p), ("len", ctypes.c_int32)]
 
 
+class NormInput(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("gamma", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("ldr", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("gamma_fp32", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class NormGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("h", ctypes.c_void_p), ("dres", ctypes.c_void_p),
+                ("gamma", ctypes.c_void_p), ("rstd", ctypes.c_void_p),
+                ("ld_dy", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+                ("ld_dres", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("gamma_fp32", ctypes.c_int32)]
+
+
+GRAD_BF16, GRAD_FP32 = 0, 1
+
+
+class GradItem(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class ClipRule(ctypes.Structure):
+    _fields_ = [("max_norm", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
@@ -87,6 +114,16 @@ _SIG = {
                                       ctypes.POINTER(Tensor), _P, _P]),
     "fp8_quantize_static_scratch": (_I32, [ctypes.POINTER(Recipe), _P, _I64, _I64, _I32, _I32,
                                            _I32, ctypes.POINTER(Tensor), _P, _P]),
+    "fp8_rmsnorm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Recipe), _I64, _I64]),
+    "fp8_rmsnorm_quantize": (_I32, [ctypes.POINTER(Recipe), ctypes.POINTER(NormInput), _I32, _I32,
+                                    _P, _P, _P, ctypes.POINTER(Tensor), _P, ctypes.c_size_t, _P,
+                                    _P]),
+    "fp8_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "fp8_rmsnorm_bwd": (_I32, [ctypes.POINTER(NormGrad), _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "fp8_grad_workspace_bytes": (ctypes.c_size_t, [_I32]),
+    "fp8_grad_norm": (_I32, [_I32, ctypes.POINTER(GradItem), ctypes.POINTER(ClipRule), _P, _P, _P,
+                             ctypes.c_size_t, _P]),
+    "fp8_grad_clip": (_I32, [_I32, ctypes.POINTER(GradItem), _P, _P]),
     "fp8_status_str": (ctypes.c_char_p, [_I32]),
     "fp8_last_cuda_error": (ctypes.c_char_p, []),
 }

@@ -367,3 +367,224 @@ def linear_dgrad_dgelu(recipe: Recipe, dy: QTensor, w: QTensor, h_q: QTensor, dh
                                     _stream(stream))
     L.check(st, "fp8_linear_dgrad_dgelu")
     return dh_q
+
+
+def _rows_2d(t: torch.Tensor, name: str):
+    """Row pitch of a bf16 [rows, cols] tensor whose rows are contiguous."""
+    if t.dtype != torch.bfloat16 or t.dim() != 2:
+        raise TypeError(f"{name}: a bf16 [rows, cols] tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    # The stride of a dimension of size one says nothing
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _like(t: Optional[torch.Tensor], shape, dtype, name: str):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)}")
+
+
+def _gamma(gamma: torch.Tensor, cols: int):
+    if gamma.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("gamma: bf16 or fp32")
+    _like(gamma, (cols,), gamma.dtype, "gamma")
+    return int(gamma.dtype == torch.float32)
+
+
+def rmsnorm_workspace_bytes(recipe: Recipe, rows, cols):
+    rc = recipe.c()
+    return int(L.load().fp8_rmsnorm_workspace_bytes(ctypes.byref(rc), rows, cols))
+
+
+def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Tensor,
+                     residual: Optional[torch.Tensor] = None, eps=1e-5, want_row=True,
+                     want_col=True, want_y=False, out: Optional[QTensor] = None,
+                     h: Optional[torch.Tensor] = None, rstd: Optional[torch.Tensor] = None,
+                     y: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, status=None, stream=None):
+    """fp8_rmsnorm_quantize: h = x + residual, RMSNorm of h and the FP8 copies of its output.
+
+    x and residual are bf16 [rows, cols], their rows may be strided; any number of rows. Returns
+    (out, h, rstd, y): `out` holds the copies of the output padded with rows of zeros to the
+    recipe's row quantum (out.rows), h the new residual stream (x itself without a residual),
+    rstd fp32 [rows] for rmsnorm_bwd, y the bf16 output (with want_y). Buffers that are not
+    given are allocated; for delayed scaling `out` is bound to its DelayedState."""
+    lib = L.load()
+    rows, cols = x.shape
+    ldx = _rows_2d(x, "x")
+    inp = L.NormInput(x.data_ptr(), None, gamma.data_ptr(), ldx, 0, rows, cols,
+                      _gamma(gamma, cols), eps)
+    _like(h, (rows, cols), torch.bfloat16, "h")
+    _like(y, (rows, cols), torch.bfloat16, "y")
+    _like(rstd, (rows,), torch.float32, "rstd")
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("residual: the shape of x")
+        inp.ldr = _rows_2d(residual, "residual")
+        inp.residual = residual.data_ptr()
+        if h is None:
+            h = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+    else:
+        h = x
+    if rstd is None:
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+    if want_y and y is None:
+        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+    rc = ct = None
+    need = 0
+    if want_row or want_col:
+        q = 128 if recipe.kind in ("mxfp8", "blockwise") else 16
+        padded = -(-rows // q) * q
+        if out is None:
+            out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
+                                device=x.device)
+        for name, shape in (("row", (padded, cols)), ("col", (cols, padded))):
+            t = getattr(out, name)
+            if (want_row if name == "row" else want_col) and (t is None or t.shape != shape):
+                raise ValueError(f"out.{name}: shape {shape} (rows padded to {padded})")
+        rc, ct = ctypes.byref(recipe.c()), out.c()
+        need = int(lib.fp8_rmsnorm_workspace_bytes(rc, rows, cols))
+        if need and (workspace is None or workspace.numel() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
+    st = lib.fp8_rmsnorm_quantize(rc, ctypes.byref(inp), int(want_row), int(want_col),
+                                  None if residual is None else h.data_ptr(), rstd.data_ptr(),
+                                  _ptr(y), None if ct is None else ctypes.byref(ct),
+                                  _ptr(workspace), 0 if workspace is None else workspace.numel(),
+                                  _ptr(status), _stream(stream))
+    L.check(st, "fp8_rmsnorm_quantize")
+    if ct is not None:
+        out.rows, out.cols, out.kind, out.role = ct.rows, ct.cols, ct.kind, ct.role
+        out.col_bf16 = ct.col_bf16
+    return out, h, rstd, y
+
+
+def rmsnorm(x: torch.Tensor, gamma: torch.Tensor, residual: Optional[torch.Tensor] = None,
+            eps=1e-5, h=None, rstd=None, y=None, stream=None):
+    """The norm alone, with a bf16 output (fp8_rmsnorm_quantize without a recipe). Returns
+    (y, h, rstd)."""
+    _, h, rstd, y = rmsnorm_quantize(None, x, gamma, residual, eps, False, False, True, h=h,
+                                     rstd=rstd, y=y, stream=stream)
+    return y, h, rstd
+
+
+def rmsnorm_bwd_workspace_bytes(rows, cols):
+    return int(L.load().fp8_rmsnorm_bwd_workspace_bytes(rows, cols))
+
+
+def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: torch.Tensor,
+                dres: Optional[torch.Tensor] = None, want_dgamma=True,
+                dh: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None, status=None, stream=None):
+    """fp8_rmsnorm_bwd: the gradient of the residual stream (of x and residual alike, `dres` the
+    gradient that reaches it past the norm) and of gamma. rstd's length is the number of rows;
+    dy may have more (linear_bwd's dx of the padded tensor): the rest is not read. Returns
+    (dh, dgamma)."""
+    lib = L.load()
+    rows, cols = rstd.numel(), h.shape[1]
+    _like(rstd, (rows,), torch.float32, "rstd")
+    if h.shape[0] != rows or dy.shape[0] < rows or dy.shape[1] != cols:
+        raise ValueError("dy, h: [rows, cols] with one row per entry of rstd")
+    inp = L.NormGrad(dy.data_ptr(), h.data_ptr(), None, gamma.data_ptr(), rstd.data_ptr(),
+                     _rows_2d(dy, "dy"), _rows_2d(h, "h"), 0, rows, cols, _gamma(gamma, cols))
+    if dres is not None:
+        if dres.shape != h.shape:
+            raise ValueError("dres: the shape of h")
+        inp.ld_dres = _rows_2d(dres, "dres")
+        inp.dres = dres.data_ptr()
+    _like(dh, (rows, cols), torch.bfloat16, "dh")
+    _like(dgamma, (cols,), torch.float32, "dgamma")
+    if dh is None:
+        dh = torch.empty((rows, cols), dtype=torch.bfloat16, device=h.device)
+    if want_dgamma:
+        if dgamma is None:
+            dgamma = torch.empty(cols, dtype=torch.float32, device=h.device)
+        need = int(lib.fp8_rmsnorm_bwd_workspace_bytes(rows, cols))
+        if need and (workspace is None or workspace.numel() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
+    else:
+        dgamma = None
+    st = lib.fp8_rmsnorm_bwd(ctypes.byref(inp), dh.data_ptr(), _ptr(dgamma), _ptr(workspace),
+                             0 if workspace is None else workspace.numel(), _ptr(status),
+                             _stream(stream))
+    L.check(st, "fp8_rmsnorm_bwd")
+    return dh, dgamma
+
+
+_GRAD_DTYPES = {torch.bfloat16: L.GRAD_BF16, torch.float32: L.GRAD_FP32}
+
+
+def _dense(t: torch.Tensor):
+    """Whether the tensor's elements fill one piece of memory, in whatever order."""
+    if t.is_contiguous():
+        return True
+    n = 1
+    for stride, size in sorted((t.stride(i), t.shape[i]) for i in range(t.dim())):
+        if size != 1 and stride != n:
+            return False
+        n *= size
+    return True
+
+
+class GradList:
+    """The gradients of a step as fp8_grad_norm and fp8_grad_clip take them: bf16 or fp32 CUDA
+    tensors of any shape, dense in memory, on one device. `outs` are the tensors that
+    grad_clip writes (the gradients themselves when not given), with the gradients' shapes and
+    strides. The list holds the tensors' addresses: it is made once for gradients that stay in
+    place, and anew for new tensors."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = self.grads if outs is None else list(outs)
+        if len(self.outs) != len(self.grads):
+            raise ValueError("outs: one tensor per gradient")
+        self.items = (L.GradItem * max(1, len(self.grads)))()
+        for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.dtype not in _GRAD_DTYPES or o.dtype not in _GRAD_DTYPES:
+                raise TypeError("gradients: bf16 or fp32")
+            if not _dense(g) or o.shape != g.shape or (o is not g and o.stride() != g.stride()):
+                raise ValueError("gradients must be dense, and outs have their shapes and strides")
+            self.items[i] = L.GradItem(g.data_ptr(), o.data_ptr(), g.numel(),
+                                       _GRAD_DTYPES[g.dtype], _GRAD_DTYPES[o.dtype])
+        self.device = self.grads[0].device if self.grads else torch.device("cuda")
+
+    def __len__(self):
+        return len(self.grads)
+
+
+def grad_workspace_bytes(n):
+    return int(L.load().fp8_grad_workspace_bytes(n))
+
+
+def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tensor] = None,
+              coef: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+              stream=None):
+    """fp8_grad_norm of a GradList (or a list of tensors): returns (norm, coef), fp32 tensors of
+    one element on the device."""
+    lib = L.load()
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    if norm is None or coef is None:
+        both = torch.empty(2, dtype=torch.float32, device=grads.device)
+        norm = both[:1] if norm is None else norm
+        coef = both[1:] if coef is None else coef
+    need = int(lib.fp8_grad_workspace_bytes(len(grads)))
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=grads.device)
+    rule = L.ClipRule(max_norm, scale)
+    st = lib.fp8_grad_norm(len(grads), grads.items, ctypes.byref(rule), norm.data_ptr(),
+                           coef.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                           _stream(stream))
+    L.check(st, "fp8_grad_norm")
+    return norm, coef
+
+
+def grad_clip(grads, coef: torch.Tensor, stream=None):
+    """fp8_grad_clip: outs = grads * coef (coef as grad_norm returns it). Returns the outs."""
+    if not isinstance(grads, GradList):
+        grads = GradList(grads)
+    if coef.dtype != torch.float32 or coef.numel() != 1:
+        raise TypeError("coef: one fp32 element")
+    st = L.load().fp8_grad_clip(len(grads), grads.items, coef.data_ptr(), _stream(stream))
+    L.check(st, "fp8_grad_clip")
+    return grads.outs

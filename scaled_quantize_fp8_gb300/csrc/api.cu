@@ -598,3 +598,198 @@ fp8_status fp8_dgelu_quantize(const fp8_recipe* recipe, const void* da_bf16,
 }
 
 }  // extern "C"
+
+// ---- RMSNorm around the linear layer, gradient norm and clipping
+
+namespace {
+constexpr int64_t kNormMaxCols = 32768;        // a row in the registers of one CTA
+constexpr int64_t kGradMaxTotal = int64_t(1) << 43;
+
+fp8_status check_pitch(int64_t ld, int64_t cols) {
+  return ld < cols || ld % 8 != 0 ? FP8_ERR_SHAPE : FP8_OK;
+}
+
+fp8_status check_norm_shape(int64_t rows, int64_t cols, int64_t quantum) {
+  if (rows < 0 || cols < 0 || cols % quantum != 0 || cols > kNormMaxCols) return FP8_ERR_SHAPE;
+  if (rows > (int64_t(1) << 40)) return FP8_ERR_SHAPE;
+  return FP8_OK;
+}
+
+fp8_status check_grads(int32_t n, const fp8_grad_item* items, bool outs) {
+  if (n < 0) return FP8_ERR_SHAPE;
+  if (n > 0 && items == nullptr) return FP8_ERR_NULL;
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    const fp8_grad_item& it = items[i];
+    if (it.numel < 0 || it.numel >= kGradMaxTotal) return FP8_ERR_SHAPE;
+    total += it.numel;
+    if (total >= kGradMaxTotal) return FP8_ERR_SHAPE;
+    for (int k = 0; k < (outs ? 2 : 1); ++k) {
+      const int32_t dt = k == 0 ? it.dtype : it.out_dtype;
+      const void* ptr = k == 0 ? it.grad : it.out;
+      if (dt != FP8_GRAD_BF16 && dt != FP8_GRAD_FP32) return FP8_ERR_UNSUPPORTED;
+      if (it.numel == 0) continue;
+      if (ptr == nullptr) return FP8_ERR_NULL;
+      if (reinterpret_cast<uintptr_t>(ptr) % (dt == FP8_GRAD_FP32 ? 4 : 2) != 0)
+        return FP8_ERR_ALIGN;
+    }
+    if (outs && it.numel > 0 && it.out == it.grad && it.dtype != it.out_dtype)
+      return FP8_ERR_UNSUPPORTED;
+  }
+  return FP8_OK;
+}
+}  // namespace
+
+extern "C" {
+
+size_t fp8_rmsnorm_workspace_bytes(const fp8_recipe* recipe, int64_t rows, int64_t cols) {
+  if (recipe == nullptr) return 0;
+  return norm_workspace_bytes(recipe->kind, rows, cols);
+}
+
+fp8_status fp8_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_norm_input* in,
+                                int32_t want_row, int32_t want_col, void* h_bf16, float* rstd,
+                                void* y_bf16, fp8_tensor* out, void* workspace, size_t ws_bytes,
+                                int32_t* dev_status, cudaStream_t stream) {
+  (void)dev_status;                         // no device-side waits in this path
+  const bool quantise = want_row || want_col;
+  if (in == nullptr) return FP8_ERR_NULL;
+  if (quantise) {
+    FP8_TRY(check_recipe(recipe));
+    if (out == nullptr) return FP8_ERR_NULL;
+  } else if (y_bf16 == nullptr) {
+    return FP8_ERR_SHAPE;                   // nothing to compute
+  }
+  const int kind = quantise ? recipe->kind : -1;
+  const int64_t rows = in->rows, cols = in->cols;
+  FP8_TRY(check_norm_shape(rows, cols, quantise ? shape_quantum(kind) : 16));
+  const int64_t rows_pad = quantise ? norm_pad_rows(kind, rows) : rows;
+  if (quantise && rows_pad * cols >= (int64_t(1) << 31)) return FP8_ERR_SHAPE;
+  if (!(in->eps >= 0.0f) || in->eps > 3.402823466e38f) return FP8_ERR_UNSUPPORTED;
+  if (in->gamma_fp32 != 0 && in->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
+  if (quantise) FP8_TRY(check_scalars(kind, out));
+  const bool col_bf16 = quantise && recipe->fp8_wgrad == 0;
+  const bool empty = rows == 0 || cols == 0;
+  if (!empty) {
+    FP8_TRY(check_ptr(in->x));
+    FP8_TRY(check_pitch(in->ldx, cols));
+    FP8_TRY(check_ptr(in->gamma));
+    if (in->residual != nullptr) {
+      FP8_TRY(check_ptr(in->residual));
+      FP8_TRY(check_pitch(in->ldr, cols));
+      FP8_TRY(check_ptr(h_bf16));
+      // in place only where h's rows lie on the input's
+      if ((h_bf16 == in->x && in->ldx != cols) || (h_bf16 == in->residual && in->ldr != cols))
+        return FP8_ERR_SHAPE;
+    }
+    if (rstd != nullptr && reinterpret_cast<uintptr_t>(rstd) % 4 != 0) return FP8_ERR_ALIGN;
+    if (y_bf16 != nullptr) FP8_TRY(check_ptr(y_bf16));
+    if (want_row) FP8_TRY(check_copy(kind, out->row, out->row_scale));
+    if (want_col) {
+      if (col_bf16) FP8_TRY(check_ptr(out->col));
+      else FP8_TRY(check_copy(kind, out->col, out->col_scale));
+    }
+    const size_t need = quantise ? norm_workspace_bytes(kind, rows, cols) : 0;
+    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
+  }
+  if (quantise) {
+    out->rows = rows_pad;
+    out->cols = cols;
+    out->role = FP8_ROLE_ACTIVATION;
+    out->kind = kind;
+    out->col_bf16 = col_bf16 ? 1 : 0;
+  }
+  if (empty) {                              // per-tensor recipes: amax 0 and its scale
+    if (!quantise) return FP8_OK;
+    return cuda_status(quantize_launch(kind, FP8_ROLE_ACTIVATION, 0, false, recipe->margin,
+                                       nullptr, 0, cols, want_row != 0, want_col != 0, col_bf16,
+                                       out, workspace, nullptr, stream));
+  }
+  NormArgs a{};
+  a.x = reinterpret_cast<const uint16_t*>(in->x);
+  a.res = reinterpret_cast<const uint16_t*>(in->residual);
+  a.gamma = in->gamma;
+  a.gamma_fp32 = in->gamma_fp32;
+  a.ldx = in->ldx;
+  a.ldr = in->ldr;
+  a.rows = rows;
+  a.cols = cols;
+  a.eps = in->eps;
+  a.h = reinterpret_cast<uint16_t*>(h_bf16);
+  a.rstd = rstd;
+  a.y = reinterpret_cast<uint16_t*>(y_bf16);
+  a.quantise = quantise;
+  if (quantise) {
+    a.kind = kind;
+    a.margin = recipe->margin;
+    a.pow2 = recipe->power_2_scales != 0;
+    a.want_row = want_row != 0;
+    a.want_col = want_col != 0;
+    a.col_bf16 = col_bf16;
+  }
+  return cuda_status(norm_quantize_launch(a, out, workspace, stream));
+}
+
+size_t fp8_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  return norm_bwd_workspace_bytes(rows, cols);
+}
+
+fp8_status fp8_rmsnorm_bwd(const fp8_norm_grad* in, void* dh_bf16, float* dgamma, void* workspace,
+                           size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  (void)dev_status;                         // no device-side waits in this path
+  if (in == nullptr) return FP8_ERR_NULL;
+  const int64_t rows = in->rows, cols = in->cols;
+  FP8_TRY(check_norm_shape(rows, cols, 16));
+  if (in->gamma_fp32 != 0 && in->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
+  if (dgamma != nullptr && !aligned16(dgamma)) return FP8_ERR_ALIGN;
+  if (cols == 0) return FP8_OK;
+  if (rows == 0)
+    return dgamma == nullptr ? FP8_OK
+                             : cuda_status(cudaMemsetAsync(dgamma, 0, size_t(cols) * 4, stream));
+  FP8_TRY(check_ptr(in->dy));
+  FP8_TRY(check_pitch(in->ld_dy, cols));
+  FP8_TRY(check_ptr(in->h));
+  FP8_TRY(check_pitch(in->ld_h, cols));
+  FP8_TRY(check_ptr(in->gamma));
+  if (in->rstd == nullptr) return FP8_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(in->rstd) % 4 != 0) return FP8_ERR_ALIGN;
+  if (in->dres != nullptr) {
+    FP8_TRY(check_ptr(in->dres));
+    FP8_TRY(check_pitch(in->ld_dres, cols));
+  }
+  FP8_TRY(check_ptr(dh_bf16));
+  if ((dh_bf16 == in->dy && in->ld_dy != cols) || (dh_bf16 == in->dres && in->ld_dres != cols))
+    return FP8_ERR_SHAPE;                   // in place only where dh's rows lie on the input's
+  const size_t need = dgamma == nullptr ? 0 : norm_bwd_workspace_bytes(rows, cols);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
+  return cuda_status(norm_bwd_launch(*in, reinterpret_cast<uint16_t*>(dh_bf16), dgamma, workspace,
+                                     stream));
+}
+
+size_t fp8_grad_workspace_bytes(int32_t n) { return grad_workspace_bytes(n); }
+
+fp8_status fp8_grad_norm(int32_t n, const fp8_grad_item* items, const fp8_clip_rule* rule,
+                         float* norm, float* coef, void* workspace, size_t ws_bytes,
+                         cudaStream_t stream) {
+  if (rule == nullptr || norm == nullptr) return FP8_ERR_NULL;
+  if (!(rule->max_norm > 0.0f)) return FP8_ERR_UNSUPPORTED;
+  if (!(rule->scale > 0.0f) || rule->scale > 3.402823466e38f) return FP8_ERR_UNSUPPORTED;
+  FP8_TRY(check_grads(n, items, false));
+  if (reinterpret_cast<uintptr_t>(norm) % 4 != 0 || reinterpret_cast<uintptr_t>(coef) % 4 != 0)
+    return FP8_ERR_ALIGN;
+  if (workspace == nullptr || ws_bytes < grad_workspace_bytes(n)) return FP8_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FP8_ERR_ALIGN;
+  return cuda_status(grad_norm_launch(n, items, *rule, norm, coef, workspace, stream));
+}
+
+fp8_status fp8_grad_clip(int32_t n, const fp8_grad_item* items, const float* coef,
+                         cudaStream_t stream) {
+  if (coef == nullptr) return FP8_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(coef) % 4 != 0) return FP8_ERR_ALIGN;
+  FP8_TRY(check_grads(n, items, true));
+  return cuda_status(grad_clip_launch(n, items, coef, stream));
+}
+
+}  // extern "C"

@@ -145,6 +145,21 @@ __device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits, float* mul
   return nan ? 0xFFu : uint32_t(e + 127);
 }
 
+// Magnitude of an fp32 value as a 31-bit pattern: ordered like the value, NaN above Inf.
+__device__ __forceinline__ uint32_t mag31(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+
+// E8M0 byte from an fp32 block amax given as its 31-bit magnitude pattern: the smallest e with
+// amax <= 448 * 2^e (e = E - 8, plus one when the mantissa exceeds 1.75), -127 below 2^-126,
+// 0xFF for an Inf/NaN block; *mult = 2^-e (1 for NaN). A finite fp32 amax never exceeds e = 120.
+__device__ __forceinline__ uint32_t mx_scale_byte_f32(uint32_t mag, float* mult) {
+  const int bexp = int(mag >> 23);
+  int e = bexp - 135 + int((mag & 0x7FFFFFu) > 0x600000u);
+  e = max(e, -127);
+  const bool nan = bexp == 0xFF;
+  *mult = nan ? 1.0f : __uint_as_float(uint32_t(127 - e) << 23);
+  return nan ? 0xFFu : uint32_t(e + 127);
+}
+
 // E8M0 byte of a power-of-two dequantisation factor 2^k, k in [-127, 127]: the float's biased
 // exponent field (2^-127, a float subnormal, has field 0, which is also its E8M0 byte).
 __device__ __forceinline__ uint32_t e8m0_of_pow2(float s_inv) {

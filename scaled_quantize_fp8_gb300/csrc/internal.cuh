@@ -126,6 +126,36 @@ cudaError_t quantize_master_launch(int kind, int margin, const float* x, int64_t
                                    bool want_row, bool want_col, fp8_tensor* out,
                                    void* workspace, cudaStream_t st);
 
+// ---- norm.cu, norm_bwd.cu (RMSNorm in front of the linear layer)
+struct NormArgs {
+  const uint16_t* x;
+  const uint16_t* res;      // or null
+  const void* gamma;
+  int gamma_fp32;
+  int64_t ldx, ldr, rows, cols;
+  float eps;
+  uint16_t* h;              // with a residual
+  float* rstd;              // or null
+  uint16_t* y;              // or null
+  bool quantise;            // false: only h, rstd and y
+  int kind, margin;
+  bool pow2, want_row, want_col, col_bf16;
+};
+size_t norm_workspace_bytes(int kind, int64_t rows, int64_t cols);
+int64_t norm_pad_rows(int kind, int64_t rows);
+cudaError_t norm_quantize_launch(const NormArgs& a, fp8_tensor* out, void* workspace,
+                                 cudaStream_t st);
+size_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+cudaError_t norm_bwd_launch(const fp8_norm_grad& a, uint16_t* dh, float* dgamma, void* workspace,
+                            cudaStream_t st);
+
+// ---- grad.cu (global gradient norm, clipping)
+size_t grad_workspace_bytes(int n);
+cudaError_t grad_norm_launch(int n, const fp8_grad_item* items, const fp8_clip_rule& rule,
+                             float* norm, float* coef, void* workspace, cudaStream_t st);
+cudaError_t grad_clip_launch(int n, const fp8_grad_item* items, const float* coef,
+                             cudaStream_t st);
+
 // ---- gemm.cu
 enum GMode : int { G_TENSOR = 0, G_MX = 1, G_BLOCK = 2, G_BF16 = 3 };
 

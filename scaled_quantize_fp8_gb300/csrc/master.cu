@@ -43,20 +43,6 @@ struct MasterParams {
 constexpr int kMLd = 132;     // padded row length of the shared tile (floats)
 constexpr uint32_t kMasterSmem = 128 * kMLd * 4;
 
-__device__ __forceinline__ uint32_t mag31(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
-
-// E8M0 byte from an fp32 block amax given as its 31-bit magnitude pattern: the smallest e with
-// amax <= 448 * 2^e (e = E - 8, plus one when the mantissa exceeds 1.75), -127 below 2^-126,
-// 0xFF for an Inf/NaN block; *mult = 2^-e (1 for NaN). A finite fp32 amax never exceeds e = 120.
-__device__ __forceinline__ uint32_t mx_scale_byte_f32(uint32_t mag, float* mult) {
-  const int bexp = int(mag >> 23);
-  int e = bexp - 135 + int((mag & 0x7FFFFFu) > 0x600000u);
-  e = max(e, -127);
-  const bool nan = bexp == 0xFF;
-  *mult = nan ? 1.0f : __uint_as_float(uint32_t(127 - e) << 23);
-  return nan ? 0xFFu : uint32_t(e + 127);
-}
-
 // 32 fp32 values times s -> 32 E4M3 codes (NaN inputs keep their sign), stored as one segment.
 __device__ __forceinline__ void encode32_store(const float* v, float s, bool has_nan,
                                                uint8_t* dst, bool lo_ok, bool hi_ok, bool v8) {
