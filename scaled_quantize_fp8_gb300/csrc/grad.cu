@@ -138,7 +138,6 @@ __device__ __forceinline__ void grad_finish(double sum, float max_norm, float sc
 template <int N>
 __global__ void __launch_bounds__(kGradThreads)
     grad_norm_kernel(const __grid_constant__ GradList<N> l, double* part) {
-  pdl_launch_dependents();
   pdl_wait();
   __shared__ double red[kGradThreads / 32];
   const uint32_t total = l.first[l.n];
@@ -177,6 +176,7 @@ __global__ void __launch_bounds__(kGradThreads)
   a.flush();
   const double s = cta_sum(a.d, red);
   if (threadIdx.x == 0) part[blockIdx.x] = s;
+  pdl_launch_dependents();
 }
 
 __global__ void __launch_bounds__(kGradThreads)
@@ -227,7 +227,6 @@ __device__ __forceinline__ void clip8(const uint8_t* src, uint8_t* dst, bool f32
 template <int N>
 __global__ void __launch_bounds__(kGradThreads)
     grad_clip_kernel(const __grid_constant__ GradList<N> l, const float* coef) {
-  pdl_launch_dependents();
   pdl_wait();
   const float k = *coef;
   const uint32_t total = l.first[l.n];
@@ -256,6 +255,7 @@ __global__ void __launch_bounds__(kGradThreads)
     const int rest = head + 8 * ng + int(threadIdx.x);
     if (rest < n) grad_put(q, o32, rest, grad_at(p, f32, rest) * k);
   }
+  pdl_launch_dependents();
 }
 
 // ------------------------------------------------------------------------- host

@@ -10,10 +10,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// h of two packed elements: bf16(x + residual), one rounding (the fp32 sum of two bf16 values
-// is rounded to bf16 only).
+// h of two packed elements: bf16(x + residual), one rounding (the packed bf16 add).
 __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
-  return pack_bf16(__fadd_rn(bf16_lo(a), bf16_lo(b)), __fadd_rn(bf16_hi(a), bf16_hi(b)));
+  const __nv_bfloat162 s = __hadd2_rn(*reinterpret_cast<const __nv_bfloat162*>(&a),
+                                      *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&s);
 }
 
 // gamma of eight consecutive columns as fp32.

@@ -34,7 +34,6 @@ struct NormBwdParams {
 template <int V, int U>
 __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ NormBwdParams p,
                                                        const int tpr) {
-  pdl_launch_dependents();
   pdl_wait();
   __shared__ float red[2][U][16];
   const int lane = threadIdx.x % tpr, grp = threadIdx.x / tpr;
@@ -146,6 +145,7 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const __grid_constant__ N
       }
     }
   }
+  pdl_launch_dependents();
 }
 
 // dgamma = sum of n partials: 16 columns (four float4) by 64 slices of the partials a CTA; the
