@@ -237,6 +237,21 @@ __device__ __forceinline__ void cp_async_16_zfill(void* smem_dst, const void* gm
                "l"(gmem_src), "r"(src_bytes)
                : "memory");
 }
+// The same with an L2 cache policy.
+__device__ __forceinline__ void cp_async_16_zfill_hint(void* smem_dst, const void* gmem_src,
+                                                       uint32_t src_bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(gmem_src), "r"(src_bytes), "l"(policy)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_16_hint(void* smem_dst, const void* gmem_src,
+                                                 uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(gmem_src), "l"(policy)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }

@@ -137,6 +137,14 @@ def test_row_copy_alone(kind, rows, cols):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols,residual", [(1500, 4096, False), (1500, 512, True),
+                                                (2500, 128, True), (300, 32768, False)])
+def test_many_rows(kind, rows, cols, residual):
+    """More rows than run at once, so that a group of threads walks several."""
+    check_norm(kind, rows, cols, residual=residual)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 def test_column_copy_alone_without_residual(kind):
     check_norm(kind, 300, 1152, residual=False, row=False)
 
