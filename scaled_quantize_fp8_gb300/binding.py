@@ -369,19 +369,27 @@ def linear_dgrad_dgelu(recipe: Recipe, dy: QTensor, w: QTensor, h_q: QTensor, dh
     return dh_q
 
 
+# The calls below run at decode rates, where Python's share counts: pointers and the stream go to
+# the library as plain integers, and structures are filled by position.
+
+def _raw_stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _rows_2d(t: torch.Tensor, name: str):
     """Row pitch of a bf16 [rows, cols] tensor whose rows are contiguous."""
     if t.dtype != torch.bfloat16 or t.dim() != 2:
         raise TypeError(f"{name}: a bf16 [rows, cols] tensor")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    (rows, cols), (pitch, step) = t.shape, t.stride()
+    if step != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    # The stride of a dimension of size one says nothing
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return pitch if rows > 1 else cols     # the stride of a dimension of size one says nothing
 
 
-def _like(t: Optional[torch.Tensor], shape, dtype, name: str):
-    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)
-                          or not t.is_contiguous()):
+def _like(t: torch.Tensor, shape, dtype, name: str):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
@@ -389,7 +397,7 @@ def _gamma(gamma: torch.Tensor, cols: int):
     if gamma.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("gamma: bf16 or fp32")
     _like(gamma, (cols,), gamma.dtype, "gamma")
-    return int(gamma.dtype == torch.float32)
+    return 1 if gamma.dtype == torch.float32 else 0
 
 
 def rmsnorm_workspace_bytes(recipe: Recipe, rows, cols):
@@ -411,48 +419,55 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
     rstd fp32 [rows] for rmsnorm_bwd, y the bf16 output (with want_y). Buffers that are not
     given are allocated; for delayed scaling `out` is bound to its DelayedState."""
     lib = L.load()
-    rows, cols = x.shape
     ldx = _rows_2d(x, "x")
+    shape = x.shape
+    rows, cols = shape
     inp = L.NormInput(x.data_ptr(), None, gamma.data_ptr(), ldx, 0, rows, cols,
                       _gamma(gamma, cols), eps)
-    _like(h, (rows, cols), torch.bfloat16, "h")
-    _like(y, (rows, cols), torch.bfloat16, "y")
-    _like(rstd, (rows,), torch.float32, "rstd")
     if residual is not None:
-        if residual.shape != x.shape:
+        if residual.shape != shape:
             raise ValueError("residual: the shape of x")
         inp.ldr = _rows_2d(residual, "residual")
         inp.residual = residual.data_ptr()
         if h is None:
-            h = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+            h = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+        else:
+            _like(h, shape, torch.bfloat16, "h")
     else:
         h = x
     if rstd is None:
         rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
-    if want_y and y is None:
-        y = torch.empty((rows, cols), dtype=torch.bfloat16, device=x.device)
+    else:
+        _like(rstd, (rows,), torch.float32, "rstd")
+    if y is not None:
+        _like(y, shape, torch.bfloat16, "y")
+    elif want_y:
+        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
     rc = ct = None
-    need = 0
     if want_row or want_col:
         q = 128 if recipe.kind in ("mxfp8", "blockwise") else 16
         padded = -(-rows // q) * q
         if out is None:
             out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
                                 device=x.device)
-        for name, shape in (("row", (padded, cols)), ("col", (cols, padded))):
-            t = getattr(out, name)
-            if (want_row if name == "row" else want_col) and (t is None or t.shape != shape):
-                raise ValueError(f"out.{name}: shape {shape} (rows padded to {padded})")
-        rc, ct = ctypes.byref(recipe.c()), out.c()
-        need = int(lib.fp8_rmsnorm_workspace_bytes(rc, rows, cols))
+        elif (want_row and (out.row is None or out.row.shape != (padded, cols))) or \
+                (want_col and (out.col is None or out.col.shape != (cols, padded))):
+            raise ValueError(f"out: copies of {padded} rows (padded) and {cols} columns")
+        ct = out.c()
+        rc = ctypes.byref(recipe.c())
+        need = lib.fp8_rmsnorm_workspace_bytes(rc, rows, cols)
         if need and (workspace is None or workspace.numel() < need):
             workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    st = lib.fp8_rmsnorm_quantize(rc, ctypes.byref(inp), int(want_row), int(want_col),
+    st = lib.fp8_rmsnorm_quantize(rc, ctypes.byref(inp), want_row, want_col,
                                   None if residual is None else h.data_ptr(), rstd.data_ptr(),
-                                  _ptr(y), None if ct is None else ctypes.byref(ct),
-                                  _ptr(workspace), 0 if workspace is None else workspace.numel(),
-                                  _ptr(status), _stream(stream))
-    L.check(st, "fp8_rmsnorm_quantize")
+                                  None if y is None else y.data_ptr(),
+                                  None if ct is None else ctypes.byref(ct),
+                                  None if workspace is None else workspace.data_ptr(),
+                                  0 if workspace is None else workspace.numel(),
+                                  None if status is None else status.data_ptr(),
+                                  _raw_stream(stream))
+    if st:
+        L.check(st, "fp8_rmsnorm_quantize")
     if ct is not None:
         out.rows, out.cols, out.kind, out.role = ct.rows, ct.cols, ct.kind, ct.role
         out.col_bf16 = ct.col_bf16
@@ -492,22 +507,27 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
             raise ValueError("dres: the shape of h")
         inp.ld_dres = _rows_2d(dres, "dres")
         inp.dres = dres.data_ptr()
-    _like(dh, (rows, cols), torch.bfloat16, "dh")
-    _like(dgamma, (cols,), torch.float32, "dgamma")
     if dh is None:
         dh = torch.empty((rows, cols), dtype=torch.bfloat16, device=h.device)
-    if want_dgamma:
+    else:
+        _like(dh, (rows, cols), torch.bfloat16, "dh")
+    if not want_dgamma:
+        dgamma = None
+    else:
         if dgamma is None:
             dgamma = torch.empty(cols, dtype=torch.float32, device=h.device)
-        need = int(lib.fp8_rmsnorm_bwd_workspace_bytes(rows, cols))
+        else:
+            _like(dgamma, (cols,), torch.float32, "dgamma")
+        need = lib.fp8_rmsnorm_bwd_workspace_bytes(rows, cols)
         if need and (workspace is None or workspace.numel() < need):
             workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
-    else:
-        dgamma = None
-    st = lib.fp8_rmsnorm_bwd(ctypes.byref(inp), dh.data_ptr(), _ptr(dgamma), _ptr(workspace),
-                             0 if workspace is None else workspace.numel(), _ptr(status),
-                             _stream(stream))
-    L.check(st, "fp8_rmsnorm_bwd")
+    st = lib.fp8_rmsnorm_bwd(ctypes.byref(inp), dh.data_ptr(),
+                             None if dgamma is None else dgamma.data_ptr(),
+                             None if workspace is None else workspace.data_ptr(),
+                             0 if workspace is None else workspace.numel(),
+                             None if status is None else status.data_ptr(), _raw_stream(stream))
+    if st:
+        L.check(st, "fp8_rmsnorm_bwd")
     return dh, dgamma
 
 
@@ -546,6 +566,7 @@ class GradList:
                 raise ValueError("gradients must be dense, and outs have their shapes and strides")
             self.items[i] = L.GradItem(g.data_ptr(), o.data_ptr(), g.numel(),
                                        _GRAD_DTYPES[g.dtype], _GRAD_DTYPES[o.dtype])
+        self.pointer = ctypes.pointer(self.items[0])
         self.device = self.grads[0].device if self.grads else torch.device("cuda")
 
     def __len__(self):
@@ -564,18 +585,19 @@ def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tens
     lib = L.load()
     if not isinstance(grads, GradList):
         grads = GradList(grads)
-    if norm is None or coef is None:
-        both = torch.empty(2, dtype=torch.float32, device=grads.device)
-        norm = both[:1] if norm is None else norm
-        coef = both[1:] if coef is None else coef
-    need = int(lib.fp8_grad_workspace_bytes(len(grads)))
+    n = len(grads.grads)
+    if norm is None:
+        norm = torch.empty(1, dtype=torch.float32, device=grads.device)
+    if coef is None:
+        coef = torch.empty(1, dtype=torch.float32, device=grads.device)
+    need = lib.fp8_grad_workspace_bytes(n)
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=grads.device)
-    rule = L.ClipRule(max_norm, scale)
-    st = lib.fp8_grad_norm(len(grads), grads.items, ctypes.byref(rule), norm.data_ptr(),
-                           coef.data_ptr(), workspace.data_ptr(), workspace.numel(),
-                           _stream(stream))
-    L.check(st, "fp8_grad_norm")
+    st = lib.fp8_grad_norm(n, grads.pointer, ctypes.byref(L.ClipRule(max_norm, scale)),
+                           norm.data_ptr(), coef.data_ptr(), workspace.data_ptr(),
+                           workspace.numel(), _raw_stream(stream))
+    if st:
+        L.check(st, "fp8_grad_norm")
     return norm, coef
 
 
@@ -585,6 +607,8 @@ def grad_clip(grads, coef: torch.Tensor, stream=None):
         grads = GradList(grads)
     if coef.dtype != torch.float32 or coef.numel() != 1:
         raise TypeError("coef: one fp32 element")
-    st = L.load().fp8_grad_clip(len(grads), grads.items, coef.data_ptr(), _stream(stream))
-    L.check(st, "fp8_grad_clip")
+    st = L.load().fp8_grad_clip(len(grads.grads), grads.pointer, coef.data_ptr(),
+                                _raw_stream(stream))
+    if st:
+        L.check(st, "fp8_grad_clip")
     return grads.outs

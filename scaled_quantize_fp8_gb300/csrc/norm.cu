@@ -61,17 +61,10 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 __device__ __forceinline__ void norm_row8(uint4 h, float rstd, const float2 (&g)[4],
                                           float2 (&y)[4]) {
   const float2 r = make_float2(rstd, rstd);
-  const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+  float2 f[4];
+  widen8(h, f);
 #pragma unroll
-  for (int k = 0; k < 4; ++k)
-    y[k] = __fmul2_rn(__fmul2_rn(make_float2(bf16_lo(w[k]), bf16_hi(w[k])), r), g[k]);
-}
-// gamma of this lane's eight columns (zeros beyond the tensor).
-__device__ __forceinline__ void gamma_pairs(const NormParams& p, int c, float2 (&g)[4]) {
-  float t[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < p.cols) load_gamma8(p.gamma, p.gamma_fp32, c, t);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) g[k] = make_float2(t[2 * k], t[2 * k + 1]);
+  for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(__fmul2_rn(f[k], r), g[k]);
 }
 __device__ __forceinline__ float max8_abs(const float2 (&y)[4]) {
   const float m = max3_abs(max3_abs(y[0].x, y[0].y, y[1].x), y[1].y, y[2].x);
@@ -186,7 +179,7 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
         g[0][2] = make_float2(b.x, b.y);
         g[0][3] = make_float2(b.z, b.w);
       } else {
-        gamma_pairs(p, 8 * v, g[0]);
+        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * v, g[0]);
       }
       return g[0];
     }
@@ -194,10 +187,11 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
   if (want_y) {
     if constexpr (kGammaRegs) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) gamma_pairs(p, 8 * (j * tpr + lane), g[j]);
+      for (int j = 0; j < V; ++j)
+        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (j * tpr + lane), g[j]);
     } else if (gamma_smem) {
       for (int v = tid; v < nv; v += nt) {
-        gamma_pairs(p, 8 * v, g[0]);
+        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * v, g[0]);
         gamma_lo[v] = make_float4(g[0][0].x, g[0][0].y, g[0][1].x, g[0][1].y);
         gamma_lo[nv + v] = make_float4(g[0][2].x, g[0][2].y, g[0][3].x, g[0][3].y);
       }
@@ -418,7 +412,7 @@ __global__ void __launch_bounds__(128, kColCtas)
   int tile = tiles_r - 1 - int(blockIdx.x) / tiles_c;
   if (tile >= 0) prefetch(tile);
   float2 g[4];
-  gamma_pairs(p, c, g);
+  gamma_pairs(p.gamma, p.gamma_fp32, p.cols, c, g);
   float scale = 1.0f;
   if constexpr (OUT == N_TENSOR) {
     uint32_t m = 0;

@@ -17,28 +17,29 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&s);
 }
 
-// gamma of eight consecutive columns as fp32.
-__device__ __forceinline__ void load_gamma8(const void* gamma, int gamma_fp32, int c, float* g) {
-  if (gamma_fp32) {
-    const float4* p = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(gamma) + c);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
-    g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
-  } else {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(
-        reinterpret_cast<const uint16_t*>(gamma) + c));
-    g[0] = bf16_lo(v.x); g[1] = bf16_hi(v.x); g[2] = bf16_lo(v.y); g[3] = bf16_hi(v.y);
-    g[4] = bf16_lo(v.z); g[5] = bf16_hi(v.z); g[6] = bf16_lo(v.w); g[7] = bf16_hi(v.w);
-  }
+// Eight bf16 as four pairs of floats.
+__device__ __forceinline__ void widen8(uint4 v, float2 (&f)[4]) {
+  f[0] = make_float2(bf16_lo(v.x), bf16_hi(v.x));
+  f[1] = make_float2(bf16_lo(v.y), bf16_hi(v.y));
+  f[2] = make_float2(bf16_lo(v.z), bf16_hi(v.z));
+  f[3] = make_float2(bf16_lo(v.w), bf16_hi(v.w));
 }
 
-// y of eight elements from their packed h.
-__device__ __forceinline__ void norm8(uint4 h, float rstd, const float* g, float* y) {
-  const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+// gamma (bf16 or fp32) of the eight columns from c on; zeros beyond the tensor.
+__device__ __forceinline__ void gamma_pairs(const void* gamma, int gamma_fp32, int cols, int c,
+                                            float2 (&g)[4]) {
+  if (c >= cols) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    y[2 * i] = __fmul_rn(__fmul_rn(bf16_lo(w[i]), rstd), g[2 * i]);
-    y[2 * i + 1] = __fmul_rn(__fmul_rn(bf16_hi(w[i]), rstd), g[2 * i + 1]);
+    for (int k = 0; k < 4; ++k) g[k] = make_float2(0.0f, 0.0f);
+  } else if (gamma_fp32) {
+    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(gamma) + c);
+    const float4 a = __ldg(q), b = __ldg(q + 1);
+    g[0] = make_float2(a.x, a.y);
+    g[1] = make_float2(a.z, a.w);
+    g[2] = make_float2(b.x, b.y);
+    g[3] = make_float2(b.z, b.w);
+  } else {
+    widen8(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(gamma) + c)), g);
   }
 }
 

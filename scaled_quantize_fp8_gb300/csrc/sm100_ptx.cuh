@@ -245,6 +245,11 @@ __device__ __forceinline__ void cp_async_16_zfill_hint(void* smem_dst, const voi
                "l"(gmem_src), "r"(src_bytes), "l"(policy)
                : "memory");
 }
+__device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gmem_src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)),
+               "l"(gmem_src)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_16_hint(void* smem_dst, const void* gmem_src,
                                                  uint64_t policy) {
   asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
