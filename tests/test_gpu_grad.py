@@ -1,6 +1,6 @@
 """GPU tests of the global gradient norm and of clipping.
 
-Tolerance of the norm: a thread adds at most 32 chunks of 8192 / 256 squares over four float32
+Tolerance of the norm: a thread adds at most 16 chunks of 16384 / 256 squares over four float32
 sums before they go to float64, 256 additions of 2^-24 relative each; half of that reaches the
 root: below NORM_RTOL. The clipped gradients are compared exactly, with the GPU's coefficient:
 one float32 product, rounded once to the output's type."""
