@@ -13,6 +13,7 @@ HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "fp8lin.h")
 HEADER_DIR = os.path.dirname(HEADER_PATH)
 
 FP8_OK = 0
+FP8_ERR_WORKSPACE = 7
 STATUS_NAMES = {0: "FP8_OK", 1: "FP8_ERR_NULL", 2: "FP8_ERR_ALIGN", 3: "FP8_ERR_SHAPE",
                 4: "FP8_ERR_UNSUPPORTED", 5: "FP8_ERR_CUDA", 6: "FP8_ERR_TIMEOUT",
                 7: "FP8_ERR_WORKSPACE"}

@@ -63,13 +63,14 @@ class QTensor:
     _c: object = field(default=None, repr=False)
 
     def c(self):
-        t = L.Tensor()
-        for name in ("row", "col", "row_scale", "col_scale", "amax", "scale", "scale_inv"):
-            v = getattr(self, name)
-            setattr(t, name, None if v is None else v.data_ptr())
-        t.rows, t.cols, t.kind, t.role = self.rows, self.cols, self.kind, self.role
-        t.col_bf16 = self.col_bf16
-        self._c = t
+        row, col, rs, cs = self.row, self.col, self.row_scale, self.col_scale
+        amax, scale, inv = self.amax, self.scale, self.scale_inv
+        self._c = t = L.Tensor(
+            None if row is None else row.data_ptr(), None if col is None else col.data_ptr(),
+            None if rs is None else rs.data_ptr(), None if cs is None else cs.data_ptr(),
+            None if amax is None else amax.data_ptr(), None if scale is None else scale.data_ptr(),
+            None if inv is None else inv.data_ptr(), self.rows, self.cols, self.kind, self.role,
+            self.col_bf16)
         return t
 
 
@@ -372,32 +373,52 @@ def linear_dgrad_dgelu(recipe: Recipe, dy: QTensor, w: QTensor, h_q: QTensor, dh
 # The calls below run at decode rates, where Python's share counts: pointers and the stream go to
 # the library as plain integers, and structures are filled by position.
 
+_BF16, _FP32 = torch.bfloat16, torch.float32
+
+
 def _raw_stream(stream):
     if stream is not None:
         return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
-def _rows_2d(t: torch.Tensor, name: str):
+def _empty(shape, dtype, device, stream):
+    """A buffer that the call makes itself, from the pool of the stream that it runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _buffer(t: Optional[torch.Tensor]):
+    """A workspace as the library takes it: address and bytes."""
+    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+
+
+def _rows_2d(t: torch.Tensor, cols, name: str):
     """Row pitch of a bf16 [rows, cols] tensor whose rows are contiguous."""
-    if t.dtype != torch.bfloat16 or t.dim() != 2:
+    if t.dtype is not _BF16 or t.dim() != 2:
         raise TypeError(f"{name}: a bf16 [rows, cols] tensor")
-    (rows, cols), (pitch, step) = t.shape, t.stride()
+    if t.is_contiguous():
+        return cols
+    pitch, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return pitch if rows > 1 else cols     # the stride of a dimension of size one says nothing
+    return pitch
 
 
 def _like(t: torch.Tensor, shape, dtype, name: str):
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
 def _gamma(gamma: torch.Tensor, cols: int):
-    if gamma.dtype not in (torch.bfloat16, torch.float32):
+    dtype = gamma.dtype
+    if dtype is not _BF16 and dtype is not _FP32:
         raise TypeError("gamma: bf16 or fp32")
-    _like(gamma, (cols,), gamma.dtype, "gamma")
-    return 1 if gamma.dtype == torch.float32 else 0
+    if gamma.shape != (cols,) or not gamma.is_contiguous():
+        raise ValueError(f"gamma: a contiguous tensor of {cols} elements")
+    return 1 if dtype is _FP32 else 0
 
 
 def rmsnorm_workspace_bytes(recipe: Recipe, rows, cols):
@@ -419,58 +440,59 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
     rstd fp32 [rows] for rmsnorm_bwd, y the bf16 output (with want_y). Buffers that are not
     given are allocated; for delayed scaling `out` is bound to its DelayedState."""
     lib = L.load()
-    ldx = _rows_2d(x, "x")
     shape = x.shape
+    if len(shape) != 2:
+        raise TypeError("x: a bf16 [rows, cols] tensor")
     rows, cols = shape
-    inp = L.NormInput(x.data_ptr(), None, gamma.data_ptr(), ldx, 0, rows, cols,
-                      _gamma(gamma, cols), eps)
+    ldx = _rows_2d(x, cols, "x")
+    ldr, res_ptr, h_ptr = 0, None, None
     if residual is not None:
         if residual.shape != shape:
             raise ValueError("residual: the shape of x")
-        inp.ldr = _rows_2d(residual, "residual")
-        inp.residual = residual.data_ptr()
+        ldr, res_ptr = _rows_2d(residual, cols, "residual"), residual.data_ptr()
         if h is None:
-            h = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+            h = _empty(shape, _BF16, x.device, stream)
         else:
-            _like(h, shape, torch.bfloat16, "h")
+            _like(h, shape, _BF16, "h")
+        h_ptr = h.data_ptr()
     else:
         h = x
     if rstd is None:
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device)
+        rstd = _empty(rows, _FP32, x.device, stream)
     else:
-        _like(rstd, (rows,), torch.float32, "rstd")
+        _like(rstd, (rows,), _FP32, "rstd")
     if y is not None:
-        _like(y, shape, torch.bfloat16, "y")
+        _like(y, shape, _BF16, "y")
     elif want_y:
-        y = torch.empty(shape, dtype=torch.bfloat16, device=x.device)
-    rc = ct = None
+        y = _empty(shape, _BF16, x.device, stream)
+    inp = L.NormInput(x.data_ptr(), res_ptr, gamma.data_ptr(), ldx, ldr, rows, cols,
+                      _gamma(gamma, cols), eps)
+    rc = out_ref = None
     if want_row or want_col:
         q = 128 if recipe.kind in ("mxfp8", "blockwise") else 16
         padded = -(-rows // q) * q
         if out is None:
-            out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
-                                device=x.device)
+            with torch.cuda.stream(stream):
+                out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
+                                    device=x.device)
         elif (want_row and (out.row is None or out.row.shape != (padded, cols))) or \
                 (want_col and (out.col is None or out.col.shape != (cols, padded))):
             raise ValueError(f"out: copies of {padded} rows (padded) and {cols} columns")
         ct = out.c()
-        rc = ctypes.byref(recipe.c())
-        need = lib.fp8_rmsnorm_workspace_bytes(rc, rows, cols)
-        if need and (workspace is None or workspace.numel() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-    st = lib.fp8_rmsnorm_quantize(rc, ctypes.byref(inp), want_row, want_col,
-                                  None if residual is None else h.data_ptr(), rstd.data_ptr(),
-                                  None if y is None else y.data_ptr(),
-                                  None if ct is None else ctypes.byref(ct),
-                                  None if workspace is None else workspace.data_ptr(),
-                                  0 if workspace is None else workspace.numel(),
-                                  None if status is None else status.data_ptr(),
-                                  _raw_stream(stream))
+        out_ref, rc = ctypes.byref(ct), ctypes.byref(recipe.c())
+    args = (rc, ctypes.byref(inp), want_row, want_col, h_ptr, rstd.data_ptr(),
+            None if y is None else y.data_ptr(), out_ref)
+    rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
+    st = lib.fp8_rmsnorm_quantize(*args, *_buffer(workspace), *rest)
+    if st == L.FP8_ERR_WORKSPACE:            # none given, or too small: one of the call's own
+        workspace = _empty(lib.fp8_rmsnorm_workspace_bytes(rc, rows, cols), torch.uint8, x.device,
+                           stream)
+        st = lib.fp8_rmsnorm_quantize(*args, *_buffer(workspace), *rest)
     if st:
         L.check(st, "fp8_rmsnorm_quantize")
-    if ct is not None:
-        out.rows, out.cols, out.kind, out.role = ct.rows, ct.cols, ct.kind, ct.role
-        out.col_bf16 = ct.col_bf16
+    if out_ref is not None:
+        out.rows, out.cols, out.kind, out.role, out.col_bf16 = (padded, cols, ct.kind, ct.role,
+                                                                ct.col_bf16)
     return out, h, rstd, y
 
 
@@ -496,36 +518,39 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
     dy may have more (linear_bwd's dx of the padded tensor): the rest is not read. Returns
     (dh, dgamma)."""
     lib = L.load()
-    rows, cols = rstd.numel(), h.shape[1]
-    _like(rstd, (rows,), torch.float32, "rstd")
-    if h.shape[0] != rows or dy.shape[0] < rows or dy.shape[1] != cols:
+    shape = h.shape
+    if len(shape) != 2 or dy.dim() != 2:
+        raise TypeError("dy, h: bf16 [rows, cols] tensors")
+    rows, cols = shape
+    _like(rstd, (rows,), _FP32, "rstd")
+    if dy.shape[0] < rows or dy.shape[1] != cols:
         raise ValueError("dy, h: [rows, cols] with one row per entry of rstd")
-    inp = L.NormGrad(dy.data_ptr(), h.data_ptr(), None, gamma.data_ptr(), rstd.data_ptr(),
-                     _rows_2d(dy, "dy"), _rows_2d(h, "h"), 0, rows, cols, _gamma(gamma, cols))
+    ld_dres, dres_ptr = 0, None
     if dres is not None:
-        if dres.shape != h.shape:
+        if dres.shape != shape:
             raise ValueError("dres: the shape of h")
-        inp.ld_dres = _rows_2d(dres, "dres")
-        inp.dres = dres.data_ptr()
+        ld_dres, dres_ptr = _rows_2d(dres, cols, "dres"), dres.data_ptr()
+    inp = L.NormGrad(dy.data_ptr(), h.data_ptr(), dres_ptr, gamma.data_ptr(), rstd.data_ptr(),
+                     _rows_2d(dy, cols, "dy"), _rows_2d(h, cols, "h"), ld_dres, rows, cols,
+                     _gamma(gamma, cols))
     if dh is None:
-        dh = torch.empty((rows, cols), dtype=torch.bfloat16, device=h.device)
+        dh = _empty(shape, _BF16, h.device, stream)
     else:
-        _like(dh, (rows, cols), torch.bfloat16, "dh")
+        _like(dh, shape, _BF16, "dh")
     if not want_dgamma:
         dgamma = None
     else:
         if dgamma is None:
-            dgamma = torch.empty(cols, dtype=torch.float32, device=h.device)
+            dgamma = _empty(cols, _FP32, h.device, stream)
         else:
-            _like(dgamma, (cols,), torch.float32, "dgamma")
-        need = lib.fp8_rmsnorm_bwd_workspace_bytes(rows, cols)
-        if need and (workspace is None or workspace.numel() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=h.device)
-    st = lib.fp8_rmsnorm_bwd(ctypes.byref(inp), dh.data_ptr(),
-                             None if dgamma is None else dgamma.data_ptr(),
-                             None if workspace is None else workspace.data_ptr(),
-                             0 if workspace is None else workspace.numel(),
-                             None if status is None else status.data_ptr(), _raw_stream(stream))
+            _like(dgamma, (cols,), _FP32, "dgamma")
+    args = (ctypes.byref(inp), dh.data_ptr(), None if dgamma is None else dgamma.data_ptr())
+    rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
+    st = lib.fp8_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
+    if st == L.FP8_ERR_WORKSPACE:
+        workspace = _empty(lib.fp8_rmsnorm_bwd_workspace_bytes(rows, cols), torch.uint8, h.device,
+                           stream)
+        st = lib.fp8_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
     if st:
         L.check(st, "fp8_rmsnorm_bwd")
     return dh, dgamma
@@ -551,7 +576,7 @@ class GradList:
     tensors of any shape, dense in memory, on one device. `outs` are the tensors that
     grad_clip writes (the gradients themselves when not given), with the gradients' shapes and
     strides. The list holds the tensors' addresses: it is made once for gradients that stay in
-    place, and anew for new tensors."""
+    place, and anew for new tensors. It also holds the results of grad_norm, `norm` and `coef`."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -568,6 +593,7 @@ class GradList:
                                        _GRAD_DTYPES[g.dtype], _GRAD_DTYPES[o.dtype])
         self.pointer = ctypes.pointer(self.items[0])
         self.device = self.grads[0].device if self.grads else torch.device("cuda")
+        self.norm, self.coef = torch.empty((2, 1), dtype=_FP32, device=self.device).unbind(0)
 
     def __len__(self):
         return len(self.grads)
@@ -581,21 +607,21 @@ def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tens
               coef: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
               stream=None):
     """fp8_grad_norm of a GradList (or a list of tensors): returns (norm, coef), fp32 tensors of
-    one element on the device."""
+    one element on the device. They are the list's own, written anew by its next grad_norm,
+    unless others are given (an allocation per call would take as long as the kernels of a
+    small list)."""
     lib = L.load()
     if not isinstance(grads, GradList):
         grads = GradList(grads)
     n = len(grads.grads)
-    if norm is None:
-        norm = torch.empty(1, dtype=torch.float32, device=grads.device)
-    if coef is None:
-        coef = torch.empty(1, dtype=torch.float32, device=grads.device)
-    need = lib.fp8_grad_workspace_bytes(n)
-    if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=grads.device)
-    st = lib.fp8_grad_norm(n, grads.pointer, ctypes.byref(L.ClipRule(max_norm, scale)),
-                           norm.data_ptr(), coef.data_ptr(), workspace.data_ptr(),
-                           workspace.numel(), _raw_stream(stream))
+    norm = grads.norm if norm is None else norm
+    coef = grads.coef if coef is None else coef
+    args = (n, grads.pointer, ctypes.byref(L.ClipRule(max_norm, scale)), norm.data_ptr(),
+            coef.data_ptr())
+    st = lib.fp8_grad_norm(*args, *_buffer(workspace), _raw_stream(stream))
+    if st == L.FP8_ERR_WORKSPACE:
+        workspace = _empty(lib.fp8_grad_workspace_bytes(n), torch.uint8, grads.device, stream)
+        st = lib.fp8_grad_norm(*args, *_buffer(workspace), _raw_stream(stream))
     if st:
         L.check(st, "fp8_grad_norm")
     return norm, coef

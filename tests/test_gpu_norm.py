@@ -432,6 +432,17 @@ def test_other_stream_and_graph():
     step(stream=side)
     side.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+    # buffers that the calls make themselves come from the given stream's pool
+    mx = F.Recipe(kind="mxfp8")
+    a = F.rmsnorm_quantize(mx, x, g, residual=res, want_y=True, stream=side)
+    da = F.rmsnorm_bwd(dy, a[1], a[2], g, stream=side)
+    side.synchronize()
+    b = F.rmsnorm_quantize(mx, x, g, residual=res, want_y=True)
+    db = F.rmsnorm_bwd(dy, b[1], b[2], g)
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(
+        (a[0].row, a[0].col, a[0].row_scale, a[0].col_scale, *a[1:], *da),
+        (b[0].row, b[0].col, b[0].row_scale, b[0].col_scale, *b[1:], *db)))
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
         step()
