@@ -268,16 +268,7 @@ __device__ __forceinline__ uint4 ldg_nc_v4_sched(const void* p) {
   return v;
 }
 
-// 16-byte load and store with an L2 cache policy, of data that other threads may write (the
-// load is not a read-only one).
-__device__ __forceinline__ uint4 ldg_v4_policy(const void* p, uint64_t policy) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.u32 {%0,%1,%2,%3}, [%4], %5;"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p), "l"(policy)
-               : "memory");
-  return v;
-}
+// 16-byte store with an L2 cache policy.
 __device__ __forceinline__ void stg_v4_policy(void* p, uint4 v, uint64_t policy) {
   asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1,%2,%3,%4}, %5;" ::"l"(p), "r"(v.x),
                "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy)

@@ -11,6 +11,13 @@
 //                     again, from L2, where the row kernel left it. With tensorwise scales,
 //                     which need the whole tensor's amax before any code, the row copy too.
 // Both evaluate y with the same two roundings, so a value has the same y in either copy.
+//
+// Bound by memory: 8192 x 4096 with a residual and both MXFP8 copies has to move 271 MB, 39.9 us
+// at the 6780 GB/s of a copy; the two kernels take 52.5 (the row kernel alone 39.0, 0.89 of that
+// rate). Why two: rstd needs a whole row, a column's scale 32 or 128 rows. One kernel that does
+// both in one pass (a cluster of CTAs with 32 or 128 whole rows in registers) took 55.7: its
+// loads, its exchange and its stores do not overlap, and no room is left to fetch the next rows
+// meanwhile. A kernel for the statistics and then one for both copies took 55.8.
 #include <algorithm>
 
 #include "common.cuh"
@@ -87,10 +94,14 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // ------------------------------------------------------------------------- rows
 // tpr threads per row (16, or a multiple of 32), V 16-byte vectors a thread; vector j of lane l
 // holds columns 8 (j tpr + l) ..  so a warp reads 512 consecutive bytes and a block of 32 (128)
-// columns lies in 4 (16) neighbouring lanes. The CTAs stay and walk the rows. Many rows take 16
-// vectors a thread, a whole row of 4096 columns to a warp: what is done per row (sums over the
-// lanes, rstd, addresses) and per block (its scale, by one of its lanes) is then spread over
-// 128 elements a thread, and no barrier stands between the rows.
+// columns lies in 4 (16) neighbouring lanes. The CTAs stay and walk the rows; each thread copies
+// its own elements of the next row to shared memory (cp.async) while it works on the present one,
+// and gamma stays in registers. Sums of squares in fp32, two a thread, then over lanes and warps
+// in a fixed order. y is made twice, for the maxima and for the codes: kept in between, it spills.
+//
+// What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 39.0 us, 6050
+// GB/s); without one the instructions as much (21.4 us for 15.0 of memory; the schedulers issue in
+// 60 % of the cycles).
 
 // Reduce the V vectors' values over the lanes that differ in the bits OFF .. 1: as long as there
 // is more than one vector, a lane passes on half of them and keeps the half that its bit names.
@@ -116,30 +127,24 @@ __device__ __forceinline__ void scatter_max(uint32_t (&m)[V]) {
   }
 }
 
-// gamma of the row kernel with eight vectors a thread: in shared memory as fp32 up to
-// kGammaSmemCols columns, the first and the second four of each vector apart so that
-// neighbouring lanes read neighbouring 16 bytes; from global memory (L1) beyond.
-constexpr int kGammaSmemCols = 8192;
-
 template <int V, int OUT, bool RES>
 __global__ void __maxnreg__(V <= 4 ? 80 : 128)
     norm_row_kernel(const __grid_constant__ NormParams p) {
-  constexpr bool kGammaRegs = V <= 4;
+  constexpr bool kGammaRegs = V <= 4;               // eight vectors: gamma comes from L1
   pdl_wait();
   __shared__ float red[2][16];
   __shared__ uint32_t redm[16];
-  extern __shared__ uint4 slots[];                  // each thread's next row, then gamma
+  extern __shared__ uint4 slots[];                  // each thread's next row
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
   const int warp = (grp * tpr + lane) >> 5, wl = (grp * tpr + lane) & 31, nv = p.cols >> 3;
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
   const bool want_y = OUT != N_STATS || p.y != nullptr || p.part != nullptr;
   // x and the residual are read once; h is read again by the column kernel (x without a
-  // residual)
+  // residual), which then finds all but 1 % of its 67 MB in L2: 53.8 us for both, 57.0 with all
+  // of it marked to be evicted first
   const uint64_t first = ptx::l2_evict_first_policy(), last = ptx::l2_evict_last_policy();
   const uint64_t xpol = RES || !p.keep_h ? first : last, hpol = p.keep_h ? last : first;
   const int nt = tpr * rpc, tid = grp * tpr + lane;
-  float4* const gamma_lo = reinterpret_cast<float4*>(slots + (RES ? 2 : 1) * V * nt);
-  const bool gamma_smem = !kGammaRegs && p.cols <= kGammaSmemCols;
 
   // Every thread copies its own elements of its next row while it works on the present one.
   const auto prefetch = [&](int64_t r) {
@@ -167,37 +172,16 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
   prefetch(int64_t(blockIdx.x) * rpc + grp);
 
   float2 g[kGammaRegs ? V : 1][4];
-  const auto gamma_of = [&](int j) -> float2(&)[4] {
-    if constexpr (kGammaRegs) {
-      return g[j];
-    } else {
-      const int v = j * tpr + lane;
-      if (gamma_smem) {
-        const float4 a = gamma_lo[min(v, nv - 1)], b = gamma_lo[nv + min(v, nv - 1)];
-        g[0][0] = make_float2(a.x, a.y);
-        g[0][1] = make_float2(a.z, a.w);
-        g[0][2] = make_float2(b.x, b.y);
-        g[0][3] = make_float2(b.z, b.w);
-      } else {
-        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * v, g[0]);
-      }
-      return g[0];
-    }
-  };
-  if (want_y) {
-    if constexpr (kGammaRegs) {
+  if (kGammaRegs && want_y) {
 #pragma unroll
-      for (int j = 0; j < V; ++j)
-        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (j * tpr + lane), g[j]);
-    } else if (gamma_smem) {
-      for (int v = tid; v < nv; v += nt) {
-        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * v, g[0]);
-        gamma_lo[v] = make_float4(g[0][0].x, g[0][0].y, g[0][1].x, g[0][1].y);
-        gamma_lo[nv + v] = make_float4(g[0][2].x, g[0][2].y, g[0][3].x, g[0][3].y);
-      }
-      __syncthreads();
-    }
+    for (int j = 0; j < V; ++j)
+      gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (j * tpr + lane), g[kGammaRegs ? j : 0]);
   }
+  const auto gamma_of = [&](int j) -> float2(&)[4] {
+    if constexpr (!kGammaRegs)
+      gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (j * tpr + lane), g[0]);
+    return g[kGammaRegs ? j : 0];
+  };
   const float tensor_scale = OUT == N_TENSOR ? *p.scale_in : 1.0f;
   uint32_t amax = 0;
   int phase = 0;
@@ -360,7 +344,12 @@ __global__ void __launch_bounds__(512) norm_amax_kernel(const uint32_t* part, in
 // copies its part of the next one to its own slots of shared memory (cp.async), row by row; the
 // 16-byte pieces of row r are exchanged by 2 (r / 8) so that four rows eight apart, as the lanes
 // read them, lie in different banks.
-constexpr int kColCtas = 5;            // per SM: 102 registers a thread
+//
+// 13.5 us at 8192 x 4096, of which its 35 MB of stores need 5: what bounds it is the length of a
+// tile's own chain (load, multiply, maxima over lanes, scale, multiply, convert) over 20 warps an
+// SM. Loads by TMA and column lines put together in shared memory took 13.3 to 13.8, bulk copies
+// 17, two tiles ahead 13.4.
+constexpr int kColCtas = 5;            // per SM: 102 registers a thread (four: +1.1 us, six: +2.4)
 
 struct NormColSmem {
   uint4 slots[4][32][8];               // each warp's part of the next tile
@@ -370,7 +359,7 @@ struct NormColSmem {
 };
 
 // FULL: nothing but the FP8 column copy is wanted and every tile lies inside the padded tensor,
-// so nothing is tested per row.
+// so nothing is tested per row (3.4 us less at 8192 x 4096, of which some are spills).
 template <int OUT, bool FULL>
 __global__ void __launch_bounds__(128, kColCtas)
     norm_col_kernel(const __grid_constant__ NormParams p, const int tiles_c, const int tiles_r) {
@@ -580,15 +569,19 @@ namespace {
 
 constexpr int kNormMaxParts = 4096;   // amax partials: one per CTA of the row kernel
 
-// Rows to stream: four vectors a thread (eight would need gamma in shared memory, and measured
-// 1.4 us slower at 8192 x 4096); one row per SM or less: as many threads as there are vectors.
-RowPlan fwd_plan(int64_t rows, int cols) {
-  return row_plan(cols, rows > num_sms() ? 4 : 1, 256);
+// Vectors a thread. One row per SM or less: one, as the row's latency counts (64 x 4096, MXFP8 row
+// copy: 2.0 us; two 2.2, four 3.0). Rows to stream: enough loads in flight, but no more registers
+// than that needs. With a residual (twice the loads) two, 4096 columns then being 256 threads
+// (8192 x 4096, both copies: 52.5 us; four 53.8, one 87.3); without one four (34.4; two 44.4); and
+// four for longer rows, of which two would make CTAs of 512 threads, one per SM
+// (4096 x 8192, row copy: 40.3; two 43.2).
+RowPlan fwd_plan(int64_t rows, int cols, bool res) {
+  return row_plan(cols, rows <= num_sms() ? 1 : res && cols <= 4096 ? 2 : 4, 256);
 }
 
 template <int OUT, bool RES>
 cudaError_t launch_rows(const NormParams& p, int* ctas, cudaStream_t st) {
-  const RowPlan pl = fwd_plan(p.rows, p.cols);
+  const RowPlan pl = fwd_plan(p.rows_pad, p.cols, RES);
   const int rpc = pl.block / pl.tpr;
   // as many CTAs as run at once (80 or 128 registers a thread)
   const int64_t grid =
@@ -599,10 +592,9 @@ cudaError_t launch_rows(const NormParams& p, int* ctas, cudaStream_t st) {
               : pl.v == 2 ? norm_row_kernel<2, OUT, RES>
               : pl.v == 4 ? norm_row_kernel<4, OUT, RES>
                           : norm_row_kernel<8, OUT, RES>;
-  const size_t smem = size_t(RES ? 2 : 1) * pl.v * pl.block * 16 +
-                      (pl.v > 4 && p.cols <= kGammaSmemCols ? size_t(p.cols) * 4 : 0);
+  const size_t smem = size_t(RES ? 2 : 1) * pl.v * pl.block * 16;
   if (smem > 47 * 1024) {                          // 48 KB with the static part
-    static ContextOnce attr[2] = {};               // v = 4 and 8 (512 threads, or gamma)
+    static ContextOnce attr[2] = {};               // v = 4 and 8, 512 threads
     const cudaError_t e = once_per_context(attr[pl.v > 4], [&] {
       return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
     });

@@ -489,3 +489,17 @@ def test_nothing_written_outside(kind, rows, cols):
         torch.cuda.synchronize()
         for big, n in held:
             assert bool((big[:guard] == 0x5A).all()) and bool((big[guard + n:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols,residual", [(300, 8192, True), (300, 5120, True),
+                                                (300, 2048, False), (160, 256, True)])
+def test_more_rows_than_sms(kind, rows, cols, residual):
+    check_norm(kind, rows, cols, residual=residual)
+
+
+@pytest.mark.parametrize("rows,cols", [(160, 1024), (610, 1040), (1300, 96), (5000, 2064),
+                                       (6000, 1024), (5000, 528)])
+def test_backward_of_many_rows(rows, cols):
+    check_bwd(rows, cols)
+    check_bwd(rows, cols, dres=False, gamma_fp32=True)
