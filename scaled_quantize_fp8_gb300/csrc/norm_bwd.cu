@@ -6,6 +6,11 @@
 // norm_bwd_kernel: a thread group holds a row, so every input is read once; each thread owns the
 // same columns in all of its rows and adds their dgamma in registers. The CTAs' sums go to
 // the workspace and norm_dgamma_kernel adds them in a fixed order.
+//
+// Bound by memory: 8 bytes an element. 8192 x 4096: 44.6 us, of which norm_dgamma_kernel 2.3; the
+// bytes alone take 39.6 at the 6780 GB/s of a copy (0.89). 2048 x 16384: 46.9, of which 5 for
+// dgamma (152 partials of 64 KB). 1024 x 32768: 76: a row of which is 192 KB of slots, so that no
+// next one is on its way while it is worked on.
 #include <algorithm>
 
 #include "common.cuh"
@@ -35,7 +40,8 @@ struct NormBwdParams {
 // shared memory while it works on the present one (cp.async; two buffers up to four vectors a
 // thread). Two passes over a row: the dot product c (and dgamma), then dh. Up to two vectors the
 // widened dy and xh stay in registers in between, beyond that they are made again from the
-// slots.
+// slots. Products and sums are fp32, two an instruction (one at a time: 39 instructions an element
+// instead of 21, 55 us at 8192 x 4096).
 template <int V, bool DRES>
 __global__ void __maxnreg__(V <= 2 ? 104 : 128)
     norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
@@ -201,7 +207,8 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
 }
 
 // dgamma = sum of n partials: 16 columns by 64 slices of the partials a CTA, a slice's loads four
-// at a time; the slices are added in a fixed order.
+// at a time; the slices are added in a fixed order. 2.3 us for 152 partials of 4096 columns, most
+// of it latency (with 304 partials, a second round of loads, 4.1).
 __global__ void __launch_bounds__(256) norm_dgamma_kernel(const float* part, int n, int cols,
                                                           float* dgamma) {
   pdl_launch_dependents();
@@ -242,14 +249,22 @@ struct BwdPlan {
   RowPlan row;
   int grid;
 };
-// Rows to stream: two vectors a thread and as many CTAs as run at once. One row per SM or less:
-// as many threads as there are vectors.
+// One CTA of up to 512 threads per SM: its row groups' dgamma meet in shared memory, so there are
+// at most as many partials as SMs (8192 x 4096: 45.3 us; with two CTAs of 256: 46.4).
+// Vectors a thread: many where loads in flight count, few where a row's latency does. Us at
+//   rows x 4096:      300    600   1200   4800   8192
+//   one              4.9    6.2   11.2   34.1   54.8
+//   two              5.9    7.1   10.6   29.0   45.3
+//   four             6.6    7.7   11.2   28.7   44.4
+// Fewer rows a CTA while there are SMs without any (600 x 1024: 3.5 us, 4.4 with full CTAs).
 BwdPlan bwd_plan(int64_t rows, int cols) {
   BwdPlan b;
-  b.row = row_plan(cols, rows > num_sms() ? 2 : 1, 256);
-  const int rpc = b.row.block / b.row.tpr;
-  const int per_sm = std::max(1, 512 / b.row.block);       // 104 registers: 512 threads per SM
-  b.grid = int(std::min<int64_t>((rows + rpc - 1) / rpc, int64_t(num_sms()) * per_sm));
+  const int sms = num_sms();
+  b.row = row_plan(cols, rows <= 4 * sms ? 1 : rows <= 32 * sms ? 2 : 4, 512);
+  int rpc = b.row.block / b.row.tpr;
+  while (rpc > 1 && (rpc / 2) * b.row.tpr >= 128 && rows <= int64_t(rpc / 2) * sms) rpc /= 2;
+  b.row.block = rpc * b.row.tpr;
+  b.grid = int(std::min<int64_t>((rows + rpc - 1) / rpc, sms));
   return b;
 }
 
