@@ -7,17 +7,22 @@
 // be captured in a graph.
 //
 // Norm: bytes read once, eight 16-byte loads a thread in flight. Squares are added in fp32 (four
-// sums a thread, at most 16 chunks each), those sums in fp64, in a fixed order. A vector whose
-// largest magnitude lies outside [2^-50, 2^50], where squares would leave fp32's range or lose
-// bits, is added in fp64 instead.
-// Clip: one multiply, read once and written once. One CTA a chunk: CTAs that stay and walk
-// chunks measured 20 us more for 134M fp32 (262 against 242 with the norm).
+// sums a thread, at most 16 chunks each), then over the warp; the warps' sums in fp64, all in a
+// fixed order. fp64 is slow on this GPU (two additions a clock and SM), hence so little of it:
+// with every thread's sum in fp64, 134M fp32 took 79.5 us instead of 77.9. A vector whose largest
+// magnitude lies outside [2^-50, 2^50], where squares would leave fp32's range or lose bits, is
+// added in fp64. 134M fp32 in 77.9 us is 6.9 TB/s: memory bound. Up to 1 MB: one launch instead of
+// two (see there).
+// Clip: one multiply, read once and written once: 134M fp32 in 153.5 us, 7.0 TB/s. One CTA a
+// chunk: CTAs that stay and walk chunks measured 20 us more (262 against 242 with the norm). Four
+// elements a thread: with eight, each fp32 sector is asked for twice.
 #include <algorithm>
 #include <cmath>
 
 #include "common.cuh"
 #include "internal.cuh"
 #include "norm.cuh"
+#include "sm100_ptx.cuh"
 
 namespace fp8lin {
 
@@ -26,6 +31,10 @@ constexpr int kGradCtas = 4;             // CTAs per SM of the norm
 constexpr int kNormChunk = 16384;        // elements a chunk of the norm
 constexpr int kClipChunk = 8192;         // ... of clipping
 constexpr int kGradUnroll = 8;           // loads in flight a thread
+constexpr int kSmallCtas = 8;            // the cluster that takes a short list
+constexpr int kSmallThreads = 512;
+constexpr int kSmallBytes = 4096;        // bytes a warp takes at once
+constexpr int kSmallPieces = 256;        // pieces at most
 constexpr int kGradFlush = 16;           // chunks between flushes of the fp32 sums
 
 // Up to N tensors in the kernel parameters (28 bytes each).
@@ -116,27 +125,73 @@ __device__ __forceinline__ void add_vec(GradSum& a, uint4 v, bool f32) {
   }
 }
 
-// Sum over the CTA in a fixed order, in thread 0.
-__device__ __forceinline__ double cta_sum(double v, double* red) {
+// Sum over the warp in a fixed order, in every lane. fp64 additions are slow (two a clock and SM),
+// so the fp32 sums are added as such; the fp64 ones only where there are any.
+__device__ __forceinline__ double warp_sum(const GradSum& a) {
+  float s = (a.s[0] + a.s[1]) + (a.s[2] + a.s[3]);
+  double d = a.d;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double t = 0.0;
-  for (int i = 0; i < int(blockDim.x >> 5); ++i) t += red[i];
-  return t;
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (__any_sync(0xffffffffu, d != 0.0)) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+  }
+  return d + double(s);
 }
 
-// norm and coef from the sum of squares; NaN and infinity pass through.
+// Sum of n doubles in shared memory, 32 to a step, by one warp.
+__device__ __forceinline__ double sum_of(const double* red, int n, int lane) {
+  double s = lane < n ? red[lane] : 0.0;
+  for (int i = 32 + lane; i < n; i += 32) s += red[i];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+// norm and coef from the sum of squares; NaN and infinity pass through. fp64 is slow here too, so
+// the root of sum = m 4^k, 1 <= m < 4, is taken in fp32 and corrected by one Newton step.
 __device__ __forceinline__ void grad_finish(double sum, float max_norm, float scale, float* norm,
                                             float* coef) {
-  const float n = float(double(scale) * sqrt(sum));
+  double root = sum;
+  if (sum > 0.0 && !isinf(sum)) {                    // no subnormal: a square is 2^-298 or more
+    const uint32_t hi = uint32_t(__double2hiint(sum)), lo = uint32_t(__double2loint(sum));
+    const int e = int(hi >> 20) - 1023, k = e >> 1;
+    const double m = __hiloint2double(int((hi & 0xFFFFFu) | uint32_t(1023 + (e & 1)) << 20),
+                                      int(lo));
+    const float r = __fsqrt_rn(float(m));
+    const double rest = fma(-double(r), double(r), m);
+    root = (double(r) + double(float(rest) / (2.0f * r))) * __hiloint2double((1023 + k) << 20, 0);
+  }
+  const float n = float(double(scale) * root);
   *norm = n;
   if (coef != nullptr) {
     float c = max_norm / (n + 1e-6f);
     if (c > 1.0f || isinf(max_norm)) c = 1.0f;
     *coef = scale * c;
   }
+}
+
+// The squares of n elements from p on, by THREADS threads (a CTA or a warp): the elements before
+// the first 16-byte boundary, whole vectors, the rest.
+template <int THREADS>
+__device__ __forceinline__ void add_chunk(GradSum& a, const uint8_t* p, bool f32, int n, int tid) {
+  const int size = f32 ? 4 : 2, per = f32 ? 4 : 8;
+  const int head = min(n, int((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / size);
+  const int nvec = (n - head) / per;
+  const uint4* v = reinterpret_cast<const uint4*>(p + head * size);
+  for (int i = tid; i < nvec; i += kGradUnroll * THREADS) {
+    uint4 w[kGradUnroll];
+#pragma unroll
+    for (int k = 0; k < kGradUnroll; ++k) {
+      const int at = i + k * THREADS;
+      w[k] = at < nvec ? ldg_nc_v4_sched(v + at) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kGradUnroll; ++k) add_vec(a, w[k], f32);
+  }
+  const int rest = head + nvec * per + tid;
+  if (tid < head) add_one(a, grad_at(p, f32, tid));
+  if (rest < n) add_one(a, grad_at(p, f32, rest));
 }
 
 template <int N>
@@ -152,33 +207,21 @@ __global__ void __launch_bounds__(kGradThreads)
     const bool f32 = (l.numel[t] & kGradF32) != 0;
     const int64_t e0 = int64_t(c - l.first[t]) * kNormChunk;
     const int n = int(min(int64_t(kNormChunk), (l.numel[t] & kNumelMask) - e0));
-    const int size = f32 ? 4 : 2, per = f32 ? 4 : 8;
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(l.g[t]) + e0 * size;
-    // elements before the first 16-byte boundary, whole vectors, the rest
-    const int head = min(n, int((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / size);
-    const int nvec = (n - head) / per;
-    const uint4* v = reinterpret_cast<const uint4*>(p + head * size);
-    for (int i = threadIdx.x; i < nvec; i += kGradUnroll * kGradThreads) {
-      uint4 w[kGradUnroll];
-#pragma unroll
-      for (int k = 0; k < kGradUnroll; ++k) {
-        const int at = i + k * kGradThreads;
-        w[k] = at < nvec ? ldg_nc_v4_sched(v + at) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int k = 0; k < kGradUnroll; ++k) add_vec(a, w[k], f32);
-    }
-    const int rest = head + nvec * per + int(threadIdx.x);
-    if (int(threadIdx.x) < head) add_one(a, grad_at(p, f32, threadIdx.x));
-    if (rest < n) add_one(a, grad_at(p, f32, rest));
+    add_chunk<kGradThreads>(
+        a, reinterpret_cast<const uint8_t*>(l.g[t]) + e0 * (f32 ? 4 : 2), f32, n, threadIdx.x);
     if (++since == kGradFlush) {
       a.flush();
       since = 0;
     }
   }
-  a.flush();
-  const double s = cta_sum(a.d, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = s;
+  const double s = warp_sum(a);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const double t = sum_of(red, kGradThreads / 32, lane);
+    if (lane == 0) part[blockIdx.x] = t;
+  }
   pdl_launch_dependents();
 }
 
@@ -187,11 +230,52 @@ __global__ void __launch_bounds__(kGradThreads)
                        float* coef) {
   pdl_launch_dependents();
   pdl_wait();
-  __shared__ double red[kGradThreads / 32];
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kGradThreads) s += part[i];
-  s = cta_sum(s, red);
-  if (threadIdx.x == 0) grad_finish(s, max_norm, scale, norm, coef);
+  __shared__ double red[kGradThreads];
+  double s = threadIdx.x < n ? part[threadIdx.x] : 0.0;
+  for (int i = threadIdx.x + kGradThreads; i < n; i += kGradThreads) s += part[i];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    s = sum_of(red, kGradThreads, threadIdx.x);
+    if (threadIdx.x == 0) grad_finish(s, max_norm, scale, norm, coef);
+  }
+}
+
+// Norm of a short list in one launch: a cluster of kSmallCtas CTAs whose warps take a piece of 4
+// KB (one round of loads) each; the warps' sums meet in the shared memory of the first CTA. The
+// pieces themselves are in the parameters: there is nothing to look up (a binary search in the
+// constant bank took 0.8 us). Latency bound: 64 tensors of 1024 in 3.0 us and one launch, 3.9 in
+// two; at 1 MB the two take the same time on the GPU (4.6 and 4.8 us), beyond it the cluster is
+// too few SMs. 16 CTAs would be 0.7 us faster at 1 MB and no faster below, and are more than a
+// cluster may count on.
+struct GradPieces {
+  const void* p[kSmallPieces];
+  uint32_t n[kSmallPieces];              // elements; bit 31: fp32
+  int total;
+};
+__global__ void __cluster_dims__(kSmallCtas) __launch_bounds__(kSmallThreads)
+    grad_norm_small_kernel(const __grid_constant__ GradPieces l, float max_norm, float scale,
+                           float* norm, float* coef) {
+  constexpr int kWarps = kSmallThreads / 32;
+  __shared__ double red[kSmallCtas * kWarps];
+  ptx::cluster_arrive_relaxed();                   // the first CTA runs: its memory is there
+  pdl_wait();
+  const int lane = threadIdx.x & 31;
+  // neighbouring pieces go to different CTAs
+  const int warp = int(threadIdx.x >> 5) * kSmallCtas + int(blockIdx.x);
+  GradSum a;
+  for (int c = warp; c < l.total; c += kSmallCtas * kWarps)
+    add_chunk<32>(a, reinterpret_cast<const uint8_t*>(l.p[c]), (l.n[c] >> 31) != 0,
+                  int(l.n[c] & 0x7FFFFFFFu), lane);
+  const double s = warp_sum(a);
+  ptx::cluster_wait();
+  if (lane == 0) ptx::st_cluster(ptx::map_to_rank(&red[warp], 0), s);
+  ptx::cluster_sync();
+  if (warp == 0) {
+    const double t = sum_of(red, kSmallCtas * kWarps, lane);
+    if (lane == 0) grad_finish(t, max_norm, scale, norm, coef);
+  }
+  pdl_launch_dependents();
 }
 
 __device__ __forceinline__ void grad_put(void* p, bool f32, int64_t i, float v) {
@@ -306,6 +390,23 @@ cudaError_t norm_lists(int n, const fp8_grad_item* items, double* part, int* par
   return cudaSuccess;
 }
 
+// The pieces of a short list; false when there are too many.
+bool grad_pieces(int n, const fp8_grad_item* items, GradPieces* l) {
+  int c = 0;
+  for (int i = 0; i < n; ++i) {
+    const bool f32 = items[i].dtype == FP8_GRAD_FP32;
+    const int size = f32 ? 4 : 2, per = kSmallBytes / size;
+    if (items[i].numel > int64_t(kSmallPieces - c) * per) return false;
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(items[i].grad);
+    for (int64_t left = items[i].numel; left > 0; left -= per, p += kSmallBytes, ++c) {
+      l->p[c] = p;
+      l->n[c] = uint32_t(std::min<int64_t>(left, per)) | (f32 ? 0x80000000u : 0u);
+    }
+  }
+  l->total = c;
+  return true;
+}
+
 template <int N>
 cudaError_t clip_lists(int n, const fp8_grad_item* items, const float* coef, cudaStream_t st) {
   for (int at = 0; at < n;) {
@@ -328,6 +429,10 @@ size_t grad_workspace_bytes(int n) {
 
 cudaError_t grad_norm_launch(int n, const fp8_grad_item* items, const fp8_clip_rule& rule,
                              float* norm, float* coef, void* workspace, cudaStream_t st) {
+  GradPieces pieces;
+  if (grad_pieces(n, items, &pieces))
+    return launch_kernel(grad_norm_small_kernel, dim3(kSmallCtas), dim3(kSmallThreads), 0, st,
+                         nullptr, pieces, rule.max_norm, rule.scale, norm, coef);
   double* part = reinterpret_cast<double*>(workspace);
   int parts = 0;
   const cudaError_t e = n <= kGradSmall ? norm_lists<kGradSmall>(n, items, part, &parts, st)

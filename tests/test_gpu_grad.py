@@ -187,3 +187,49 @@ def test_offsets_past_32_bits():
     want = (torch.tensor(2.0 ** -10) * coef.cpu()).to(BF16)
     assert torch.equal(g[-2:].cpu(), want.expand(2)) and torch.equal(g[:2].cpu(), want.expand(2))
     assert bool((g == want.cuda()).all())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+@pytest.mark.parametrize("bytes_", [(1 << 20) - 4, 1 << 20, (1 << 20) + 4])
+@pytest.mark.parametrize("tensors", [1, 3])
+def test_short_and_long_lists(dtype, bytes_, tensors):
+    """Lists just below, at and above 1 MB, where one launch becomes two; split unevenly and at
+    odd offsets."""
+    n = bytes_ // (2 if dtype == BF16 else 4)
+    sizes = [n] if tensors == 1 else [n - 5001, 1, 5000]
+    c, _ = check(_grads(sizes, dtype, packed=True), max_norm=1e9)
+    check(_grads(sizes, dtype, packed=True), max_norm=c / 2)
+
+
+@pytest.mark.parametrize("count", [255, 256, 257])
+def test_tiny_tensors_of_both_types(count):
+    """As many tensors as a short list has room for, one less and one more."""
+    grads = _grads([1 + i % 3 for i in range(count)], BF16, packed=True)
+    grads[::2] = [g.float() for g in grads[::2]]
+    check(grads, max_norm=1e-3)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32])
+def test_range_and_not_finite_in_long_lists(dtype):
+    for sigma in (1e-25, 1e17):
+        check(_grads([700001, 3], dtype, sigma=sigma), max_norm=1.0)
+    mixed = _grads([700001], dtype, sigma=1e-25) + _grads([600000], dtype, sigma=1.0)
+    check(mixed, max_norm=1.0)
+    for bad in (math.inf, math.nan):
+        grads = _grads([700001, 3], dtype)
+        grads[0][654321] = bad
+        n, c = F.grad_norm(grads, max_norm=1.0)
+        assert math.isnan(n.item()) if math.isnan(bad) else (n.item() == bad and c.item() == 0)
+
+
+def test_norm_of_one_element():
+    """The root over float32's whole range: the square's rounding and the mantissa's count half
+    in the root, which is rounded itself, and so is its product with the scale: 3 * 2^-24."""
+    values = [3.4e38, 1.5, 1.0, 2.0, math.sqrt(2), 3.0, 0.1, 7e-4, 1e-14, 9e-16, 2.0 ** -63, 1e-30,
+              2.0 ** -126]
+    for v in values:
+        for scale in (1.0, 0.25):
+            g = torch.full((1,), v, device="cuda")
+            norm, _ = F.grad_norm([g], max_norm=1.0, scale=scale)
+            ref = g.double().item() * scale
+            assert abs(norm.item() - ref) <= 3 * 2.0 ** -24 * ref + 2.0 ** -149
