@@ -412,6 +412,14 @@ def _like(t: torch.Tensor, shape, dtype, name: str):
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
+def _on_gpu(*tensors):
+    """The tensors that a call reads or writes (None among them) must lie on the GPU: the library
+    sees addresses only."""
+    for t in tensors:
+        if t is not None and not t.is_cuda:
+            raise TypeError("CUDA tensors wanted")
+
+
 def _gamma(gamma: torch.Tensor, cols: int):
     dtype = gamma.dtype
     if dtype is not _BF16 and dtype is not _FP32:
@@ -480,6 +488,7 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
             raise ValueError(f"out: copies of {padded} rows (padded) and {cols} columns")
         ct = out.c()
         out_ref, rc = ctypes.byref(ct), ctypes.byref(recipe.c())
+    _on_gpu(x, gamma, residual, h, rstd, y, workspace)
     args = (rc, ctypes.byref(inp), want_row, want_col, h_ptr, rstd.data_ptr(),
             None if y is None else y.data_ptr(), out_ref)
     rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
@@ -544,6 +553,7 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
             dgamma = _empty(cols, _FP32, h.device, stream)
         else:
             _like(dgamma, (cols,), _FP32, "dgamma")
+    _on_gpu(dy, h, rstd, gamma, dres, dh, dgamma, workspace)
     args = (ctypes.byref(inp), dh.data_ptr(), None if dgamma is None else dgamma.data_ptr())
     rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
     st = lib.fp8_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
@@ -592,6 +602,7 @@ class GradList:
             self.items[i] = L.GradItem(g.data_ptr(), o.data_ptr(), g.numel(),
                                        _GRAD_DTYPES[g.dtype], _GRAD_DTYPES[o.dtype])
         self.pointer = ctypes.pointer(self.items[0])
+        self.on_gpu = all(t.is_cuda for t in self.grads + self.outs)
         self.device = self.grads[0].device if self.grads else torch.device("cuda")
         self.norm, self.coef = torch.empty((2, 1), dtype=_FP32, device=self.device).unbind(0)
 
@@ -601,6 +612,12 @@ class GradList:
 
 def grad_workspace_bytes(n):
     return int(L.load().fp8_grad_workspace_bytes(n))
+
+
+def _scalar(t: torch.Tensor, name: str):
+    if t.dtype is not _FP32 or t.numel() != 1:
+        raise TypeError(f"{name}: one fp32 element")
+    return t
 
 
 def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tensor] = None,
@@ -614,8 +631,11 @@ def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tens
     if not isinstance(grads, GradList):
         grads = GradList(grads)
     n = len(grads.grads)
-    norm = grads.norm if norm is None else norm
-    coef = grads.coef if coef is None else coef
+    norm = grads.norm if norm is None else _scalar(norm, "norm")
+    coef = grads.coef if coef is None else _scalar(coef, "coef")
+    if not grads.on_gpu:
+        raise TypeError("gradients: CUDA tensors wanted")
+    _on_gpu(norm, coef, workspace)
     args = (n, grads.pointer, ctypes.byref(L.ClipRule(max_norm, scale)), norm.data_ptr(),
             coef.data_ptr())
     st = lib.fp8_grad_norm(*args, *_buffer(workspace), _raw_stream(stream))
@@ -631,8 +651,9 @@ def grad_clip(grads, coef: torch.Tensor, stream=None):
     """fp8_grad_clip: outs = grads * coef (coef as grad_norm returns it). Returns the outs."""
     if not isinstance(grads, GradList):
         grads = GradList(grads)
-    if coef.dtype != torch.float32 or coef.numel() != 1:
-        raise TypeError("coef: one fp32 element")
+    _scalar(coef, "coef")
+    if not grads.on_gpu or not coef.is_cuda:
+        raise TypeError("gradients and coef: CUDA tensors wanted")
     st = L.load().fp8_grad_clip(len(grads.grads), grads.pointer, coef.data_ptr(),
                                 _raw_stream(stream))
     if st:

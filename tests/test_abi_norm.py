@@ -230,3 +230,19 @@ def test_binding_refusals():
     with pytest.raises(TypeError):
         binding.grad_clip([x], torch.zeros(1, dtype=torch.float64))
     assert len(binding.GradList([x, x.t(), torch.zeros(3, 5, 7).permute(2, 0, 1)])) == 3
+
+
+def test_binding_refuses_cpu_tensors():
+    """Well-formed calls on CPU tensors: the library would take their addresses for the GPU's."""
+    x, g = torch.zeros(4, 256, dtype=torch.bfloat16), torch.ones(256)
+    out = torch.empty_like(x)
+    with pytest.raises(TypeError):
+        binding.rmsnorm(x, g, y=out)
+    with pytest.raises(TypeError):
+        binding.rmsnorm_bwd(x, x, torch.ones(4), g)
+    with pytest.raises(TypeError):
+        binding.grad_norm([x])
+    with pytest.raises(TypeError):
+        binding.grad_clip([x], torch.ones(1))
+    with pytest.raises(TypeError):
+        binding.grad_norm([x], norm=torch.zeros(2))
