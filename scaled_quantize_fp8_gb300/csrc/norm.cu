@@ -140,7 +140,7 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
   const bool want_y = OUT != N_STATS || p.y != nullptr || p.part != nullptr;
   // x and the residual are read once; h is read again by the column kernel (x without a
-  // residual), which then finds all but 1 % of its 67 MB in L2: 53.8 us for both, 57.0 with all
+  // residual), which then finds all but 1 % of its 67 MB in L2: 52.6 us for both, 55.7 with all
   // of it marked to be evicted first
   const uint64_t first = ptx::l2_evict_first_policy(), last = ptx::l2_evict_last_policy();
   const uint64_t xpol = RES || !p.keep_h ? first : last, hpol = p.keep_h ? last : first;
@@ -334,38 +334,41 @@ __global__ void __launch_bounds__(512) norm_amax_kernel(const uint32_t* part, in
 }
 
 // ------------------------------------------------------------------------- columns
-// A CTA of four warps, one below the other, walks tiles of 128 rows x 64 columns of one column
-// block. Lane l of a warp has the eight columns 8 (l / 4) .. of the eight rows 8 (l % 4) .. of
-// its 32: y stays in 64 registers between the maxima and the codes, and the column copy is
-// written in 8-byte pieces, four neighbouring lanes to a 32-byte sector, four warps to a
-// 128-byte line (with the lanes the other way round, sectors from lanes 8 apart, the stores took
-// twice the time). Column maxima over a warp are reduced by halving: at each step a lane passes
-// on half of its columns and keeps the other half. While a tile is worked on, the warp already
-// copies its part of the next one to its own slots of shared memory (cp.async), row by row; the
-// 16-byte pieces of row r are exchanged by 2 (r / 8) so that four rows eight apart, as the lanes
-// read them, lie in different banks.
+// A CTA of four warps, side by side, walks tiles of 128 rows x 64 columns of one column block.
+// Lane l of a warp has the eight columns 8 (l / 16) .. of its 16 and the eight rows 8 (l % 16) ..:
+// y stays in 64 registers between the maxima and the codes, and 16 lanes write 128 bytes of a
+// column at once. Column maxima over lanes are reduced by halving: at each step a lane passes on
+// half of its columns and keeps the other half. While a tile is worked on, the CTA copies the next
+// one to the other buffer in shared memory (cp.async); the 16-byte pieces of row r are exchanged
+// by (r / 8) % 8 so that the rows eight apart that lanes read at once lie in different banks.
 //
-// 13.5 us at 8192 x 4096, of which its 35 MB of stores need 5: what bounds it is the length of a
-// tile's own chain (load, multiply, maxima over lanes, scale, multiply, convert) over 20 warps an
-// SM. Loads by TMA and column lines put together in shared memory took 13.3 to 13.8, bulk copies
-// 17, two tiles ahead 13.4.
-constexpr int kColCtas = 5;            // per SM: 102 registers a thread (four: +1.1 us, six: +2.4)
+// 13.6 us at 8192 x 4096 (MXFP8), where its 35 MB of stores alone would take 5. No one resource
+// bounds it: L1, the ALUs and the schedulers are each about half busy; without its loads it takes
+// 3 us less, without its stores 4 less. Loads by TMA, two tiles ahead, column lines put together
+// in shared memory, a warp's rows one below the other: all within 0.5 us.
+//
+// CTAs per SM: five, at 102 registers a thread (MXFP8: 52.6 us for both copies; four 52.9, six,
+// which spill, 54.6), but six where there are no maxima (FULL, per-tensor scales: 49.5; five
+// 50.0).
+template <int OUT, bool FULL>
+constexpr int col_ctas() {
+  return OUT == N_TENSOR && FULL ? 6 : 5;
+}
 
 struct NormColSmem {
-  uint4 slots[4][32][8];               // each warp's part of the next tile
-  alignas(16) float rstd[4][32];       // of each warp's rows
-  uint2 cmax[4][32];                   // 1x128: column maxima of each warp's rows
+  uint4 slots[2][128][8];
+  alignas(16) float rstd[2][128];
   uint32_t red[4];
 };
 
 // FULL: nothing but the FP8 column copy is wanted and every tile lies inside the padded tensor,
-// so nothing is tested per row (3.4 us less at 8192 x 4096, of which some are spills).
+// so nothing is tested per row (8192 x 4096, both copies: 52.6 us, else 55.4, with a few spills).
 template <int OUT, bool FULL>
-__global__ void __launch_bounds__(128, kColCtas)
+__global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
     norm_col_kernel(const __grid_constant__ NormParams p, const int tiles_c, const int tiles_r) {
   __shared__ NormColSmem S;
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, l8 = lane >> 2, l4 = lane & 3;
-  const int c0 = (int(blockIdx.x) % tiles_c) * 64, c = c0 + 8 * l8;
+  const int t = threadIdx.x, lane = t & 31, w = t >> 5, l2 = lane >> 4, l16 = lane & 15;
+  const int c0 = (int(blockIdx.x) % tiles_c) * 64, c = c0 + 16 * w + 8 * l2;
   const int step = int(gridDim.x) / tiles_c;
   const bool in = FULL || c < p.cols;
   const bool want_row = !FULL && OUT == N_TENSOR && p.row != nullptr;
@@ -373,46 +376,45 @@ __global__ void __launch_bounds__(128, kColCtas)
   pdl_wait();
 
   const uint64_t policy = ptx::l2_evict_first_policy();          // the last read of h
-  float next_rstd = 0.0f;
-  const auto prefetch = [&](int tile) {
-    // lane l copies piece l % 8 of the rows l / 8, l / 8 + 4, ..
-    const int64_t r0 = int64_t(tile) * 128 + 32 * w, r = r0 + (lane >> 3);
-    const int piece = lane & 7, cp = c0 + 8 * piece;
+  const auto prefetch = [&](int tile, int buf) {
+    // thread t copies piece t % 8 of the rows t / 8, t / 8 + 16, ..
+    const int64_t r0 = int64_t(tile) * 128, r = r0 + (t >> 3);
+    const int piece = t & 7, cp = c0 + 8 * piece;
     const uint16_t* x = p.h + r * p.ldx + cp;
-    const bool whole = cp < p.cols && r0 + 32 <= p.rows;
+    const bool whole = cp < p.cols && r0 + 128 <= p.rows;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int row = (lane >> 3) + 4 * i;
-      uint4* d = &S.slots[w][row][piece ^ (2 * (i >> 1))];
+      const int row = (t >> 3) + 16 * i;
+      uint4* d = &S.slots[buf][row][piece ^ ((row >> 3) & 7)];
       if (whole) {
         ptx::cp_async_16_hint(d, x, policy);
       } else {                                                   // nothing read beyond: zeros
-        const uint32_t n = cp < p.cols && r + 4 * i < p.rows ? 16u : 0u;
+        const uint32_t n = cp < p.cols && r + 16 * i < p.rows ? 16u : 0u;
         ptx::cp_async_16_zfill_hint(d, n ? x : p.h, n, policy);
       }
-      x += 4 * p.ldx;
+      x += 16 * p.ldx;
     }
     ptx::cp_async_commit();
     // padding rows: rstd 0, so that y = (0 0) gamma = 0
-    next_rstd = r0 + lane < p.rows ? p.rstd[r0 + lane] : 0.0f;
+    return r0 + t < p.rows ? p.rstd[r0 + t] : 0.0f;
   };
 
   // Last tiles first: the row kernel wrote the last rows of h most recently.
   int tile = tiles_r - 1 - int(blockIdx.x) / tiles_c;
-  if (tile >= 0) prefetch(tile);
+  float next_rstd = tile >= 0 ? prefetch(tile, 0) : 0.0f;
   float2 g[4];
   gamma_pairs(p.gamma, p.gamma_fp32, p.cols, c, g);
   float scale = 1.0f;
   if constexpr (OUT == N_TENSOR) {
     uint32_t m = 0;
     if (p.scale_in == nullptr || blockIdx.x == 0) {
-      for (int i = threadIdx.x; i < p.n_part; i += 128) m = max(m, p.part[i]);
+      for (int i = t; i < p.n_part; i += 128) m = max(m, p.part[i]);
       m = cta_max(m, S.red);
     }
     float sinv;
     scale = p.scale_in != nullptr ? *p.scale_in
                                   : scale_from_amax(__uint_as_float(m), p.margin, &sinv);
-    if (blockIdx.x == 0 && threadIdx.x == 0) {
+    if (blockIdx.x == 0 && t == 0) {
       *p.amax_out = __uint_as_float(m);
       if (p.scale_in == nullptr) {
         *p.scale_out = scale;
@@ -421,21 +423,21 @@ __global__ void __launch_bounds__(128, kColCtas)
     }
   }
 
-  for (; tile >= 0; tile -= step) {
-    const int64_t r0 = int64_t(tile) * 128 + 32 * w, r = r0 + 8 * l4;
-    S.rstd[w][lane] = next_rstd;
+  for (int buf = 0; tile >= 0; tile -= step, buf ^= 1) {
+    const int64_t r0 = int64_t(tile) * 128, r = r0 + 8 * l16;
+    S.rstd[buf][t] = next_rstd;
     ptx::cp_async_wait<0>();
-    __syncwarp();
+    __syncthreads();                               // the tile is there, the last one read
+    if (tile >= step) next_rstd = prefetch(tile - step, buf ^ 1);
     float2 y[8][4];
     {
-      const float4 ra = *reinterpret_cast<const float4*>(&S.rstd[w][8 * l4]);
-      const float4 rb = *reinterpret_cast<const float4*>(&S.rstd[w][8 * l4 + 4]);
+      const float4 ra = *reinterpret_cast<const float4*>(&S.rstd[buf][8 * l16]);
+      const float4 rb = *reinterpret_cast<const float4*>(&S.rstd[buf][8 * l16 + 4]);
       const float rs[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i) norm_row8(S.slots[w][8 * l4 + i][l8 ^ (2 * l4)], rs[i], g, y[i]);
+      for (int i = 0; i < 8; ++i)
+        norm_row8(S.slots[buf][8 * l16 + i][(2 * w + l2) ^ (l16 & 7)], rs[i], g, y[i]);
     }
-    __syncwarp();
-    if (tile >= step) prefetch(tile - step);
 
     // ---- the columns' multipliers
     float2 cs[4];
@@ -461,30 +463,26 @@ __global__ void __launch_bounds__(128, kColCtas)
 #pragma unroll
       for (int k = 0; k < 2; ++k)
         m[k] = max(v ? m[k + 2] : m[k], __shfl_xor_sync(0xffffffffu, v ? m[k] : m[k + 2], 1));
-      const int c2 = c + 2 * l4;                       // this lane's two columns
+      const int c2 = c + 2 * (lane & 3);               // this lane's two columns
       float s0, s1;
       if constexpr (OUT == N_MX) {
         const uint32_t b0 = mx_scale_byte_f32(m[0], &s0), b1 = mx_scale_byte_f32(m[1], &s1);
         uint8_t* d = reinterpret_cast<uint8_t*>(p.col_scale) +
-                     mx_scale_offset(c2, r0 >> 5, p.rows_pad);
+                     mx_scale_offset(c2, r >> 5, p.rows_pad);
         if (want_col && in) {
           d[0] = uint8_t(b0);
           d[16] = uint8_t(b1);                         // the next column's row of the atom
         }
       } else {
-        S.cmax[w][lane] = make_uint2(m[0], m[1]);
-        __syncthreads();                               // the four warps' 128 rows
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint2 o = S.cmax[k][lane];
-          m[0] = max(m[0], o.x);
-          m[1] = max(m[1], o.y);
+        for (int k = 0; k < 2; ++k) {                  // 128 rows
+          m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], 4));
+          m[k] = max(m[k], __shfl_xor_sync(0xffffffffu, m[k], 8));
         }
-        __syncthreads();                               // the next tile's may be written
         float i0, i1;
         s0 = scale_from_amax(__uint_as_float(m[0]), p.margin, &i0, 448.0f, p.pow2);
         s1 = scale_from_amax(__uint_as_float(m[1]), p.margin, &i1, 448.0f, p.pow2);
-        if (want_col && in && w == 0) {
+        if (want_col && in && l16 < 4) {
           if (p.pow2) {
             uint8_t* d = reinterpret_cast<uint8_t*>(p.col_scale) +
                          mx_scale_offset(c2, r0 >> 5, p.rows_pad);
@@ -535,14 +533,24 @@ __global__ void __launch_bounds__(128, kColCtas)
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i][k] = __fmul2_rn(y[i][k], cs[k]);
     }
-    if (want_row && stored) {
-      uint8_t* row = p.row + r * p.cols + c;
+    if (want_row) {
+      // by way of the tile's buffer (64 bytes a row, 8-byte units exchanged like the pieces), so
+      // that four lanes write 64 consecutive bytes
+      __syncthreads();
+      uint2* codes = reinterpret_cast<uint2*>(&S.slots[buf][0][0]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        *reinterpret_cast<uint2*>(row) =
+      for (int i = 0; i < 8; ++i)
+        codes[(8 * l16 + i) * 8 + ((2 * w + l2) ^ (l16 & 7))] =
             make_uint2(cvt_e4m3x4(y[i][0].x, y[i][0].y, y[i][1].x, y[i][1].y),
                        cvt_e4m3x4(y[i][2].x, y[i][2].y, y[i][3].x, y[i][3].y));
-        row += p.cols;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int q = (t >> 2) + 32 * i, e = (q >> 3) & 7, at = 2 * (t & 3);
+        const uint4 v = reinterpret_cast<const uint4*>(codes)[(q * 8 + (at ^ (e & 6))) >> 1];
+        if (r0 + q < p.rows_pad && c0 + 8 * at < p.cols)
+          *reinterpret_cast<uint4*>(p.row + (r0 + q) * p.cols + c0 + 8 * at) =
+              (e & 1) ? make_uint4(v.z, v.w, v.x, v.y) : v;
       }
     }
     if (want_col && !col_bf16 && stored) {
@@ -613,11 +621,12 @@ template <int OUT>
 cudaError_t launch_cols(const NormParams& p, cudaStream_t st) {
   const int tiles_c = (p.cols + 63) / 64;
   const int tiles_r = int((p.rows_pad + 127) / 128);
-  // every CTA keeps its column block (and gamma): a whole number of CTAs per block
-  const int per_block = std::min(tiles_r, std::max(1, num_sms() * kColCtas / tiles_c));
   const bool full = (OUT != N_TENSOR || p.row == nullptr) && p.col != nullptr && !p.col_bf16 &&
                     p.cols % 64 == 0 && p.rows_pad % 128 == 0;
   auto kern = full ? norm_col_kernel<OUT, true> : norm_col_kernel<OUT, false>;
+  // every CTA keeps its column block (and gamma): a whole number of CTAs per block
+  const int ctas = full ? col_ctas<OUT, true>() : col_ctas<OUT, false>();
+  const int per_block = std::min(tiles_r, std::max(1, num_sms() * ctas / tiles_c));
   return launch_kernel(kern, dim3(unsigned(per_block * tiles_c)), dim3(128), 0, st, nullptr, p,
                        tiles_c, tiles_r);
 }
