@@ -1029,6 +1029,45 @@ def run_reference(args):
     }), flush=True)
 
 
+def norm_cases(torch, F):
+    """The norm's and the gradients' kernels at the MLP's sizes: name -> (one launch, bytes that it
+    has to move). x or residual, h, row and column copy; dy, h, dres, dh; the gradients twice."""
+    M, K, Fd = TOKENS, HIDDEN, FFN
+    g = torch.Generator(device="cuda").manual_seed(0)
+
+    def randn(*shape, dtype=torch.bfloat16):
+        return torch.randn(shape, device="cuda", generator=g).to(dtype)
+
+    x, res, dy, gamma = randn(M, K), randn(M, K), randn(M, K), randn(K)
+    h, dh, rstd = torch.empty_like(x), torch.empty_like(x), torch.empty(M, device="cuda")
+    cases = {}
+    for kind in ("mxfp8", "tensorwise", "blockwise", "delayed"):
+        rec = F.Recipe(kind=kind)
+        out = F.empty_qtensor(rec, M, K, "activation")
+        ws = torch.empty(F.rmsnorm_workspace_bytes(rec, M, K), dtype=torch.uint8, device="cuda")
+        scales = {"mxfp8": 2 / 32.0, "blockwise": 2 * 4 / 128.0}.get(kind, 0.0)
+
+        def run(rec=rec, out=out, ws=ws):
+            F.rmsnorm_quantize(rec, x, gamma, residual=res, out=out, h=h, rstd=rstd, workspace=ws)
+
+        cases[f"norm_{kind}"] = (run, M * K * (8 + scales))
+    ws = torch.empty(F.rmsnorm_bwd_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    dgamma = torch.empty(K, device="cuda")
+    cases["norm_mxfp8"][0]()                                  # h and rstd
+    cases["norm_bwd"] = (lambda: F.rmsnorm_bwd(dy, h, rstd, gamma, dres=res, dh=dh, dgamma=dgamma,
+                                               workspace=ws), M * K * 8)
+    grads = [randn(Fd, K, dtype=torch.float32), randn(K, Fd, dtype=torch.float32)]
+    grads = F.GradList(grads, [torch.empty_like(t) for t in grads])   # in place: clipped once only
+    gws = torch.empty(F.grad_workspace_bytes(2), dtype=torch.uint8, device="cuda")
+
+    def clip():
+        norm, coef = F.grad_norm(grads, max_norm=1.0, workspace=gws)
+        F.grad_clip(grads, coef)
+
+    cases["grad"] = (clip, 2 * Fd * K * 12)
+    return cases
+
+
 def run_profile_case(args):
     """Launch one kernel kind a few times on its own (for ncu captures; prints no JSON line).
     quant_mx / quant_tensorwise / quant_blockwise: X --rows x --cols bf16 (default 16384 x 8192,
@@ -1042,7 +1081,10 @@ def run_profile_case(args):
     dgrad, fc1 wgrad) at full size, in that order.
     quant_group_mx: the MLP step's grouped MXFP8 quantize of X 8192 x 4096, W1 16384 x 4096
     and W2 4096 x 16384 (one launch); quant_group_blockwise: the same three tensors under the
-    blockwise recipe (X in 1x128 blocks, W1 and W2 in 128x128 tiles)."""
+    blockwise recipe (X in 1x128 blocks, W1 and W2 in 128x128 tiles).
+    norm_mx / norm_tensorwise / norm_blockwise / norm_delayed: RMSNorm with a residual and both
+    FP8 copies, 8192 x 4096; norm_bwd: its backward pass; grad: gradient norm, then clipping, of
+    the fp32 gradients of the MLP's two weights (134M elements)."""
     import torch
     import scaled_quantize_fp8_gb300 as F
     from scaled_quantize_fp8_gb300 import build as B
@@ -1107,6 +1149,10 @@ def run_profile_case(args):
         dw = torch.empty((4096, 4096), dtype=torch.bfloat16, device="cuda")
         for _ in range(args.steps):
             F.linear_bwd(rec, dyq, xq, None, want_dx=False, dw=dw)
+    elif case.startswith("norm") or case == "grad":
+        run = norm_cases(torch, F)[case.replace("_mx", "_mxfp8")][0]
+        for _ in range(args.steps):
+            run()
     elif case.startswith("quant"):
         R, C = args.rows, args.cols
         x = torch.randn((R, C), device="cuda", generator=g).to(torch.bfloat16)
@@ -1253,8 +1299,9 @@ def run_targets(args):
 
 def run_kernels(args):
     """Per-recipe kernel timings (prints one JSON object; not the benchmark line): quantize of an
-    8192 x 4096 bf16 activation (row + column copies) and the fprop GEMM 8192 x 4096 x 4096 and
-    4096^3, each the mean of 20 launches timed with CUDA events after 5 warm-up launches."""
+    8192 x 4096 bf16 activation (row + column copies), the fprop GEMM 8192 x 4096 x 4096 and
+    4096^3, and the norm's and the gradients' kernels, each the mean of 20 launches timed with
+    CUDA events after 5 warm-up launches."""
     import torch
     import scaled_quantize_fp8_gb300 as F
     from scaled_quantize_fp8_gb300 import build as B
@@ -1322,6 +1369,10 @@ def run_kernels(args):
     ms = timed(lambda: F.quantize_master(rec, w32, out=qm))
     out["quantize_master_mxfp8_16384x4096"] = {
         "ms": round(ms, 4), "GB/s": round(16384 * 4096 * (4 + 2 + 2 / 32.0) / ms / 1e6, 1)}
+    # RMSNorm with FP8 copies, its backward pass, gradient norm and clipping
+    for name, (run, n) in norm_cases(torch, F).items():
+        ms = timed(run)
+        out[name] = {"ms": round(ms, 4), "GB/s": round(n / ms / 1e6, 1)}
     torch.cuda.synchronize()
     print(json.dumps({"kernels": out}), flush=True)
 
@@ -1334,7 +1385,8 @@ def main():
                              "gemm_mx",
                              "gemm_tensorwise", "gemm_blockwise", "gelu_mx", "dgelu_mx",
                              "gemm_gelu_mx", "gemm_dgelu_mx", "gemm_mx_mlp",
-                             "gemm_wgrad_blockwise", "suite"])
+                             "gemm_wgrad_blockwise", "norm_mx", "norm_tensorwise",
+                             "norm_blockwise", "norm_delayed", "norm_bwd", "grad", "suite"])
     ap.add_argument("--rows", type=int, default=16384, help="--profile quant_*: tensor rows")
     ap.add_argument("--cols", type=int, default=8192, help="--profile quant_*: tensor columns")
     ap.add_argument("--gpus", type=int, default=1)
