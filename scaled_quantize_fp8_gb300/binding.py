@@ -31,9 +31,18 @@ class Recipe:
     power_2_scales: bool = False
 
     def c(self):
-        return L.Recipe(KINDS[self.kind], 0 if self.format == "e4m3" else 1, int(self.margin),
-                        int(self.amax_history_len), 0 if self.amax_compute_algo == "max" else 1,
-                        1 if self.fp8_wgrad else 0, 1 if self.power_2_scales else 0)
+        """The library's form; kept until a field changes."""
+        kept = self.__dict__.get("_c")
+        if kept is None:
+            kept = L.Recipe(KINDS[self.kind], 0 if self.format == "e4m3" else 1, int(self.margin),
+                            int(self.amax_history_len), 0 if self.amax_compute_algo == "max" else 1,
+                            1 if self.fp8_wgrad else 0, 1 if self.power_2_scales else 0)
+            self.__dict__["_c"] = kept
+        return kept
+
+    def __setattr__(self, name, value):
+        self.__dict__.pop("_c", None)
+        self.__dict__[name] = value
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -392,7 +401,7 @@ def _empty(shape, dtype, device, stream):
 
 def _buffer(t: Optional[torch.Tensor]):
     """A workspace as the library takes it: address and bytes."""
-    return (None, 0) if t is None else (t.data_ptr(), t.numel() * t.element_size())
+    return (None, 0) if t is None else (t.data_ptr(), t.nbytes)
 
 
 def _rows_2d(t: torch.Tensor, cols, name: str):
@@ -412,12 +421,9 @@ def _like(t: torch.Tensor, shape, dtype, name: str):
         raise ValueError(f"{name}: a contiguous {dtype} tensor of shape {tuple(shape)}")
 
 
-def _on_gpu(*tensors):
-    """The tensors that a call reads or writes (None among them) must lie on the GPU: the library
-    sees addresses only."""
-    for t in tensors:
-        if t is not None and not t.is_cuda:
-            raise TypeError("CUDA tensors wanted")
+def _not_on_gpu():
+    """The library sees addresses only, so every tensor of a call must lie on the GPU."""
+    raise TypeError("CUDA tensors wanted")
 
 
 def _gamma(gamma: torch.Tensor, cols: int):
@@ -453,7 +459,7 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
         raise TypeError("x: a bf16 [rows, cols] tensor")
     rows, cols = shape
     ldx = _rows_2d(x, cols, "x")
-    ldr, res_ptr, h_ptr = 0, None, None
+    ldr, res_ptr, h_ptr = 0, 0, None
     if residual is not None:
         if residual.shape != shape:
             raise ValueError("residual: the shape of x")
@@ -473,8 +479,8 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
         _like(y, shape, _BF16, "y")
     elif want_y:
         y = _empty(shape, _BF16, x.device, stream)
-    inp = L.NormInput(x.data_ptr(), res_ptr, gamma.data_ptr(), ldx, ldr, rows, cols,
-                      _gamma(gamma, cols), eps)
+    inp = L.pack_norm_input(x.data_ptr(), res_ptr, gamma.data_ptr(), ldx, ldr, rows, cols,
+                            _gamma(gamma, cols), eps)
     rc = out_ref = None
     if want_row or want_col:
         q = 128 if recipe.kind in ("mxfp8", "blockwise") else 16
@@ -488,8 +494,11 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
             raise ValueError(f"out: copies of {padded} rows (padded) and {cols} columns")
         ct = out.c()
         out_ref, rc = ctypes.byref(ct), ctypes.byref(recipe.c())
-    _on_gpu(x, gamma, residual, h, rstd, y, workspace)
-    args = (rc, ctypes.byref(inp), want_row, want_col, h_ptr, rstd.data_ptr(),
+    if not (x.is_cuda and gamma.is_cuda and h.is_cuda and rstd.is_cuda
+            and (residual is None or residual.is_cuda) and (y is None or y.is_cuda)
+            and (workspace is None or workspace.is_cuda)):
+        _not_on_gpu()
+    args = (rc, inp, want_row, want_col, h_ptr, rstd.data_ptr(),
             None if y is None else y.data_ptr(), out_ref)
     rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
     st = lib.fp8_rmsnorm_quantize(*args, *_buffer(workspace), *rest)
@@ -534,14 +543,14 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
     _like(rstd, (rows,), _FP32, "rstd")
     if dy.shape[0] < rows or dy.shape[1] != cols:
         raise ValueError("dy, h: [rows, cols] with one row per entry of rstd")
-    ld_dres, dres_ptr = 0, None
+    ld_dres, dres_ptr = 0, 0
     if dres is not None:
         if dres.shape != shape:
             raise ValueError("dres: the shape of h")
         ld_dres, dres_ptr = _rows_2d(dres, cols, "dres"), dres.data_ptr()
-    inp = L.NormGrad(dy.data_ptr(), h.data_ptr(), dres_ptr, gamma.data_ptr(), rstd.data_ptr(),
-                     _rows_2d(dy, cols, "dy"), _rows_2d(h, cols, "h"), ld_dres, rows, cols,
-                     _gamma(gamma, cols))
+    inp = L.pack_norm_grad(dy.data_ptr(), h.data_ptr(), dres_ptr, gamma.data_ptr(),
+                           rstd.data_ptr(), _rows_2d(dy, cols, "dy"), _rows_2d(h, cols, "h"),
+                           ld_dres, rows, cols, _gamma(gamma, cols))
     if dh is None:
         dh = _empty(shape, _BF16, h.device, stream)
     else:
@@ -553,8 +562,11 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
             dgamma = _empty(cols, _FP32, h.device, stream)
         else:
             _like(dgamma, (cols,), _FP32, "dgamma")
-    _on_gpu(dy, h, rstd, gamma, dres, dh, dgamma, workspace)
-    args = (ctypes.byref(inp), dh.data_ptr(), None if dgamma is None else dgamma.data_ptr())
+    if not (dy.is_cuda and h.is_cuda and rstd.is_cuda and gamma.is_cuda and dh.is_cuda
+            and (dres is None or dres.is_cuda) and (dgamma is None or dgamma.is_cuda)
+            and (workspace is None or workspace.is_cuda)):
+        _not_on_gpu()
+    args = (inp, dh.data_ptr(), None if dgamma is None else dgamma.data_ptr())
     rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
     st = lib.fp8_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
     if st == L.FP8_ERR_WORKSPACE:
@@ -633,10 +645,10 @@ def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tens
     n = len(grads.grads)
     norm = grads.norm if norm is None else _scalar(norm, "norm")
     coef = grads.coef if coef is None else _scalar(coef, "coef")
-    if not grads.on_gpu:
-        raise TypeError("gradients: CUDA tensors wanted")
-    _on_gpu(norm, coef, workspace)
-    args = (n, grads.pointer, ctypes.byref(L.ClipRule(max_norm, scale)), norm.data_ptr(),
+    if not (grads.on_gpu and norm.is_cuda and coef.is_cuda
+            and (workspace is None or workspace.is_cuda)):
+        _not_on_gpu()
+    args = (n, grads.pointer, L.pack_clip_rule(max_norm, scale), norm.data_ptr(),
             coef.data_ptr())
     st = lib.fp8_grad_norm(*args, *_buffer(workspace), _raw_stream(stream))
     if st == L.FP8_ERR_WORKSPACE:
@@ -652,8 +664,8 @@ def grad_clip(grads, coef: torch.Tensor, stream=None):
     if not isinstance(grads, GradList):
         grads = GradList(grads)
     _scalar(coef, "coef")
-    if not grads.on_gpu or not coef.is_cuda:
-        raise TypeError("gradients and coef: CUDA tensors wanted")
+    if not (grads.on_gpu and coef.is_cuda):
+        _not_on_gpu()
     st = L.load().fp8_grad_clip(len(grads.grads), grads.pointer, coef.data_ptr(),
                                 _raw_stream(stream))
     if st:
