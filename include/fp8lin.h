@@ -401,14 +401,18 @@ size_t fp8_rmsnorm_workspace_bytes(const fp8_recipe *recipe, int64_t rows, int64
  *   out        the copies of y padded with rows of zeros to a multiple of the recipe's row
  *              quantum q (128 for MXFP8 and BLOCKWISE, 16 otherwise): out->rows is that padded
  *              count, the buffers hold it, and the padding's codes and scales are those of
- *              zeros, so a GEMM of the padded tensor can follow. A padded size of 2^31 elements or more is
- *              refused. DELAYED reads out->scale and writes out->amax (fp8_amax_update follows);
- *              TENSORWISE writes amax, scale and scale_inv.
+ *              zeros (for a finite gamma), so a GEMM of the padded tensor can follow. A padded
+ *              size of 2^31 elements or more is refused. DELAYED reads out->scale and writes
+ *              out->amax (fp8_amax_update follows); TENSORWISE writes amax, scale and scale_inv.
  *   workspace  fp8_rmsnorm_workspace_bytes() of device scratch.
- * NaN in y gives code 0x7F; an Inf or NaN anywhere in a row reaches the whole row. Apart from h
- * no output may overlap an input. Source: the norm in front of each linear layer of the
- * transformer block that the "Low-Precision Training Guide" trains (section "When to Use Low
- * Precision"); the formulas and the fusion are this library's.
+ *   dev_status is not written: nothing in these kernels waits for anything that could fail to
+ *              come. The same holds for fp8_rmsnorm_bwd.
+ * NaN in y gives code 0x7F. A NaN in a row of h makes the whole row NaN. An infinity, or squares
+ * whose sum leaves fp32's range (|h| of 2^63 and more), make the row's rstd 0: its finite elements
+ * become zeros, the infinite ones NaN. Apart from h no output may overlap an input.
+ * Source: the norm in front of each linear layer of the transformer block that the "Low-Precision
+ * Training Guide" trains (section "When to Use Low Precision"); the formulas and the fusion are
+ * this library's.
  */
 fp8_status fp8_rmsnorm_quantize(const fp8_recipe *recipe, const fp8_norm_input *in,
                                 int32_t want_row, int32_t want_col, void *h_bf16, float *rstd,
@@ -417,7 +421,8 @@ fp8_status fp8_rmsnorm_quantize(const fp8_recipe *recipe, const fp8_norm_input *
 
 /* Inputs of the norm's backward pass; pointers and pitches as for fp8_norm_input. */
 typedef struct {
-  const void *dy;        /* [rows][cols] bf16: the gradient of y (fp8_linear_bwd's dx), pitch ld_dy */
+  const void *dy;        /* [rows][cols] bf16: the gradient of y (fp8_linear_bwd's dx), pitch
+                            ld_dy */
   const void *h;         /* [rows][cols] bf16: the stream the norm read, pitch ld_h */
   const void *dres;      /* [rows][cols] bf16: the gradient of h on the residual path, pitch
                             ld_dres, or NULL */
