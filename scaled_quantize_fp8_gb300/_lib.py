@@ -39,6 +39,8 @@ class Tensor(ctypes.Structure):
                 ("col_bf16", ctypes.c_int32)]
 
 
+pack_tensor = struct.Struct("@PPPPPPPqqiii").pack_into      # into a Tensor
+
 QUANTIZE_GROUP_MAX = 4
 
 

@@ -74,11 +74,12 @@ class QTensor:
     def c(self):
         row, col, rs, cs = self.row, self.col, self.row_scale, self.col_scale
         amax, scale, inv = self.amax, self.scale, self.scale_inv
-        self._c = t = L.Tensor(
-            None if row is None else row.data_ptr(), None if col is None else col.data_ptr(),
-            None if rs is None else rs.data_ptr(), None if cs is None else cs.data_ptr(),
-            None if amax is None else amax.data_ptr(), None if scale is None else scale.data_ptr(),
-            None if inv is None else inv.data_ptr(), self.rows, self.cols, self.kind, self.role,
+        self._c = t = L.Tensor()
+        L.pack_tensor(                               # half the time of the fields as arguments
+            t, 0, 0 if row is None else row.data_ptr(), 0 if col is None else col.data_ptr(),
+            0 if rs is None else rs.data_ptr(), 0 if cs is None else cs.data_ptr(),
+            0 if amax is None else amax.data_ptr(), 0 if scale is None else scale.data_ptr(),
+            0 if inv is None else inv.data_ptr(), self.rows, self.cols, self.kind, self.role,
             self.col_bf16)
         return t
 

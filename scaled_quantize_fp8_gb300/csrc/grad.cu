@@ -48,6 +48,9 @@ struct GradList {
 };
 constexpr int64_t kGradF32 = int64_t(1) << 62, kOutF32 = int64_t(1) << 61;
 constexpr int64_t kNumelMask = kOutF32 - 1;
+// Two lengths of the list: 64 tensors are 1.8 KB of parameters, 1024 are 29 KB (of 32 that a launch
+// may have), which costs the host 0.75 us a launch (grad_clip of 12 tensors: 3.4 against 4.15) and
+// the GPU 0.1.
 constexpr int kGradSmall = 64, kGradLarge = 1024;
 
 // The tensor that holds chunk c.
