@@ -97,7 +97,8 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // columns lies in 4 (16) neighbouring lanes. The CTAs stay and walk the rows; each thread copies
 // its own elements of the next row to shared memory (cp.async) while it works on the present one,
 // and gamma stays in registers. Sums of squares in fp32, two a thread, then over lanes and warps
-// in a fixed order. y is made twice, for the maxima and for the codes: kept in between, it spills.
+// in a fixed order. y is made twice, for the maxima and for the codes: kept in between, two vectors
+// are no faster (39.0 us either way) and four spill.
 //
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 39.0 us, 6050
 // GB/s); without one the instructions as much (21.4 us for 15.0 of memory; the schedulers issue in
