@@ -129,7 +129,7 @@ __device__ __forceinline__ void scatter_max(uint32_t (&m)[V]) {
 }
 
 template <int V, int OUT, bool RES>
-__global__ void __maxnreg__(V <= 4 ? 80 : 128)
+__global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     norm_row_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kGammaRegs = V <= 4;               // eight vectors: gamma comes from L1
   pdl_wait();
@@ -592,10 +592,12 @@ template <int OUT, bool RES>
 cudaError_t launch_rows(const NormParams& p, int* ctas, cudaStream_t st) {
   const RowPlan pl = fwd_plan(p.rows_pad, p.cols, RES);
   const int rpc = pl.block / pl.tpr;
-  // as many CTAs as run at once (80 or 128 registers a thread)
+  // as many CTAs as run at once: a quarter of an SM has registers for seven warps at 72 a thread,
+  // six at 80, four at 128. One CTA too many per SM runs alone at the end (6528 x 5120, row copy:
+  // 46 us instead of 40).
   const int64_t grid =
       std::min<int64_t>((p.rows_pad + rpc - 1) / rpc,
-                        int64_t(num_sms()) * std::max(1, (pl.v <= 4 ? 800 : 512) / pl.block));
+                        int64_t(num_sms()) * std::max(1, (pl.v <= 2 ? 896 : pl.v == 4 ? 768 : 512) / pl.block));
   if (ctas != nullptr) *ctas = int(grid);
   auto kern = pl.v == 1   ? norm_row_kernel<1, OUT, RES>
               : pl.v == 2 ? norm_row_kernel<2, OUT, RES>
