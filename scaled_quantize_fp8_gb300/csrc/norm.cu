@@ -13,7 +13,7 @@
 // Both evaluate y with the same two roundings, so a value has the same y in either copy.
 //
 // Bound by memory: 8192 x 4096 with a residual and both MXFP8 copies has to move 271 MB, 39.9 us
-// at the 6780 GB/s of a copy; the two kernels take 52.5 (the row kernel alone 39.0, 0.89 of that
+// at the 6780 GB/s of a copy; the two kernels take 52.2 (the row kernel alone 38.8, 0.90 of that
 // rate). Why two: rstd needs a whole row, a column's scale 32 or 128 rows. One kernel that does
 // both in one pass (a cluster of CTAs with 32 or 128 whole rows in registers) took 55.7: its
 // loads, its exchange and its stores do not overlap, and no room is left to fetch the next rows
@@ -101,8 +101,8 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // are no faster (39.0 us either way) and four spill.
 //
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 39.0 us, 6050
-// GB/s); without one the instructions as much (21.4 us for 15.0 of memory; the schedulers issue in
-// 60 % of the cycles).
+// GB/s); without one the instructions as much (19.4 us for 15.0 of memory; 32-bit offsets and sums
+// read four at a time gave 1.1 of the 20.5 before).
 
 // Reduce the V vectors' values over the lanes that differ in the bits OFF .. 1: as long as there
 // is more than one vector, a lane passes on half of them and keeps the half that its bit names.
@@ -133,7 +133,7 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     norm_row_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kGammaRegs = V <= 4;               // eight vectors: gamma comes from L1
   pdl_wait();
-  __shared__ float red[2][16];
+  __shared__ alignas(16) float red[2][16];
   __shared__ uint32_t redm[16];
   extern __shared__ uint4 slots[];                  // each thread's next row
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
@@ -226,8 +226,16 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     if (warps > 1) {
       if ((lane & 31) == 0) red[phase][warp] = ss;
       __syncthreads();
+      const float* q = red[phase] + grp * warps;
       ss = 0.0f;
-      for (int i = 0; i < warps; ++i) ss += red[phase][grp * warps + i];
+      if ((warps & 3) == 0) {
+        for (int i = 0; i < warps; i += 4) {
+          const float4 a = *reinterpret_cast<const float4*>(q + i);
+          ss += (a.x + a.y) + (a.z + a.w);
+        }
+      } else {
+        for (int i = 0; i < warps; ++i) ss += q[i];
+      }
       phase ^= 1;               // the next row's sums go to the other buffer: one barrier a row
     }
     const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
@@ -264,7 +272,7 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
       const int j = V >= 4 ? T * q + s : V == 2 ? q >> 1 : 0, v = j * tpr + (lane & ~15);
       if (stored && v < nv && (V >= 4 ? s < T : s == 0 && (V == 2 ? (q & 1) == 0 : q == 0)))
         *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
-                                     mx_scale_offset(r, v >> 2, p.cols)) = word;
+                                     mx_scale_offset32(r, v >> 2, p.cols)) = word;
     }
     if constexpr (OUT == N_BW) {
       scatter_max<V, 8>(m);
@@ -274,7 +282,7 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
       if (stored && v < nv && (lane & 15) % (16 / V) == 0) {
         if (p.pow2)
           *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
-                                       mx_scale_offset(r, v >> 2, p.cols)) =
+                                       mx_scale_offset32(r, v >> 2, p.cols)) =
               e8m0_of_pow2(sinv) * 0x01010101u;
         else
           reinterpret_cast<float*>(p.row_scale)[int64_t(v >> 4) * p.rows_pad + r] = sinv;
@@ -282,7 +290,9 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     }
 
     // ---- codes
-    uint8_t* row = OUT == N_STATS ? nullptr : p.row + r * p.cols + 8 * lane;
+    // (a quantised tensor has less than 2^31 elements)
+    uint8_t* row =
+        OUT == N_STATS ? nullptr : p.row + (uint32_t(r) * uint32_t(p.cols) + uint32_t(8 * lane));
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int v = j * tpr + lane;
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(512) norm_amax_kernel(const uint32_t* part, in
 // one to the other buffer in shared memory (cp.async); the 16-byte pieces of row r are exchanged
 // by (r / 8) % 8 so that the rows eight apart that lanes read at once lie in different banks.
 //
-// 13.6 us at 8192 x 4096 (MXFP8), where its 35 MB of stores alone would take 5. No one resource
+// 13.4 us at 8192 x 4096 (MXFP8), where its 35 MB of stores alone would take 5. No one resource
 // bounds it: L1, the ALUs and the schedulers are each about half busy; without its loads it takes
 // 3 us less, without its stores 4 less. Loads by TMA, two tiles ahead, column lines put together
 // in shared memory, a warp's rows one below the other: all within 0.5 us.
@@ -555,17 +565,18 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
       }
     }
     if (want_col && !col_bf16 && stored) {
-      uint8_t* col = p.col + int64_t(c) * p.rows_pad + r;
+      const uint32_t pitch = uint32_t(p.rows_pad);    // (less than 2^31 elements)
+      uint32_t at = uint32_t(c) * pitch + uint32_t(r);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        *reinterpret_cast<uint2*>(col) =
+        *reinterpret_cast<uint2*>(p.col + at) =
             make_uint2(cvt_e4m3x4(y[0][k].x, y[1][k].x, y[2][k].x, y[3][k].x),
                        cvt_e4m3x4(y[4][k].x, y[5][k].x, y[6][k].x, y[7][k].x));
-        col += p.rows_pad;
-        *reinterpret_cast<uint2*>(col) =
+        at += pitch;
+        *reinterpret_cast<uint2*>(p.col + at) =
             make_uint2(cvt_e4m3x4(y[0][k].y, y[1][k].y, y[2][k].y, y[3][k].y),
                        cvt_e4m3x4(y[4][k].y, y[5][k].y, y[6][k].y, y[7][k].y));
-        col += p.rows_pad;
+        at += pitch;
       }
     }
   }

@@ -43,6 +43,12 @@ __device__ __forceinline__ void gamma_pairs(const void* gamma, int gamma_fp32, i
   }
 }
 
+// mx_scale_offset of a tensor with less than 2^31 elements, in 32 bits.
+__device__ __forceinline__ uint32_t mx_scale_offset32(uint32_t r, uint32_t kb, uint32_t cols) {
+  return ((r >> 7) * (cols >> 7) + (kb >> 2)) * 512u + (r & 31u) * 16u + ((r & 127u) >> 5) * 4u +
+         (kb & 3u);
+}
+
 // Threads per row and vectors (eight columns) a thread for the kernels that keep a row in the
 // registers of one thread group: at most 512 threads, 16 or a multiple of 32, and no more
 // vectors than that needs.
