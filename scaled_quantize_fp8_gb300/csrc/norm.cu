@@ -91,14 +91,14 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
   return m;
 }
 
-// ------------------------------------------------------------------------- rows
-// tpr threads per row (16, or a multiple of 32), V 16-byte vectors a thread; vector j of lane l
-// holds columns 8 (j tpr + l) ..  so a warp reads 512 consecutive bytes and a block of 32 (128)
-// columns lies in 4 (16) neighbouring lanes. The CTAs stay and walk the rows; each thread copies
-// its own elements of the next row to shared memory (cp.async) while it works on the present one,
-// and gamma stays in registers. Sums of squares in fp32, two a thread, then over lanes and warps
-// in a fixed order. y is made twice, for the maxima and for the codes: kept in between, two vectors
-// are no faster (39.0 us either way) and four spill.
+// ------------------------------------------------------------------------- rows tpr threads per
+// row (16, or a multiple of 32), V 16-byte vectors a thread; vector j of lane l holds columns 8 (j
+// tpr + l) ..  so a warp reads 512 consecutive bytes and a block of 32 (128) columns lies in 4
+// (16) neighbouring lanes. The CTAs stay and walk the rows; each thread copies its own elements of
+// the next row to shared memory (cp.async) while it works on the present one, and gamma stays in
+// registers. Sums of squares in fp32, two a thread, then over lanes and warps in a fixed order. y
+// is made twice, for the maxima and for the codes: kept in between, two vectors are no faster
+// (39.0 us either way) and four spill.
 //
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 39.0 us, 6050
 // GB/s); without one the instructions as much (19.4 us for 15.0 of memory; 32-bit offsets and sums
@@ -128,6 +128,15 @@ __device__ __forceinline__ void scatter_max(uint32_t (&m)[V]) {
   }
 }
 
+// Rows on their way while one is worked on: as many as make four vectors a thread. 131072 x 256
+// (one vector): both MXFP8 copies with a residual 0.67 -> 0.75 of the measured bandwidth, delayed
+// ones without 0.50 -> 0.61; more than four vectors are no faster (two rows of 4096 columns with a
+// residual: 41.6 us instead of 38.9).
+template <int V, bool RES>
+__host__ __device__ constexpr int rows_ahead() {
+  return V == 1 ? (RES ? 2 : 4) : V == 2 && !RES ? 2 : 1;
+}
+
 template <int V, int OUT, bool RES>
 __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     norm_row_kernel(const __grid_constant__ NormParams p) {
@@ -135,7 +144,7 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
   pdl_wait();
   __shared__ alignas(16) float red[2][16];
   __shared__ uint32_t redm[16];
-  extern __shared__ uint4 slots[];                  // each thread's next row
+  extern __shared__ uint4 slots[];                  // each thread's next rows
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
   const int warp = (grp * tpr + lane) >> 5, wl = (grp * tpr + lane) & 31, nv = p.cols >> 3;
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
@@ -146,31 +155,40 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
   const uint64_t first = ptx::l2_evict_first_policy(), last = ptx::l2_evict_last_policy();
   const uint64_t xpol = RES || !p.keep_h ? first : last, hpol = p.keep_h ? last : first;
   const int nt = tpr * rpc, tid = grp * tpr + lane;
+  constexpr int kAhead = rows_ahead<V, RES>();
 
   // Every thread copies its own elements of its next row while it works on the present one.
-  const auto prefetch = [&](int64_t r) {
+  const auto prefetch = [&](int64_t r, int buf) {
+    uint4* s = slots + buf * (RES ? 2 : 1) * V * nt + tid;
     const uint16_t* x = p.x + r * p.ldx + 8 * lane;
     const uint16_t* res = RES ? p.res + r * p.ldr + 8 * lane : nullptr;
     if (V * tpr == nv && r < p.rows) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        ptx::cp_async_16_hint(slots + j * nt + tid, x + 8 * j * tpr, xpol);
-        if (RES) ptx::cp_async_16_hint(slots + (V + j) * nt + tid, res + 8 * j * tpr, first);
+        ptx::cp_async_16_hint(s + j * nt, x + 8 * j * tpr, xpol);
+        if (RES) ptx::cp_async_16_hint(s + (V + j) * nt, res + 8 * j * tpr, first);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) {                  // nothing read beyond the tensor: zeros
         const bool in = r < p.rows && j * tpr + lane < nv;
         const uint32_t n = in ? 16u : 0u;
-        ptx::cp_async_16_zfill_hint(slots + j * nt + tid, in ? x + 8 * j * tpr : p.x, n, xpol);
+        ptx::cp_async_16_zfill_hint(s + j * nt, in ? x + 8 * j * tpr : p.x, n, xpol);
         if (RES)
-          ptx::cp_async_16_zfill_hint(slots + (V + j) * nt + tid, in ? res + 8 * j * tpr : p.res,
+          ptx::cp_async_16_zfill_hint(s + (V + j) * nt, in ? res + 8 * j * tpr : p.res,
                                       n, first);
       }
     }
     ptx::cp_async_commit();
   };
-  prefetch(int64_t(blockIdx.x) * rpc + grp);
+  const int64_t row_step = int64_t(gridDim.x) * rpc;
+  prefetch(int64_t(blockIdx.x) * rpc + grp, 0);
+#pragma unroll
+  for (int k = 1; k < kAhead; ++k) {
+    const int64_t r0 = int64_t(blockIdx.x) * rpc + k * row_step;
+    if (r0 < p.rows_pad) prefetch(r0 + grp, k);
+    else ptx::cp_async_commit();                    // groups are counted: an empty one
+  }
 
   float2 g[kGammaRegs ? V : 1][4];
   if (kGammaRegs && want_y) {
@@ -185,8 +203,8 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
   };
   const float tensor_scale = OUT == N_TENSOR ? *p.scale_in : 1.0f;
   uint32_t amax = 0;
-  int phase = 0;
-  for (int64_t r0 = int64_t(blockIdx.x) * rpc; r0 < p.rows_pad; r0 += int64_t(gridDim.x) * rpc) {
+  int phase = 0, buf = 0;
+  for (int64_t r0 = int64_t(blockIdx.x) * rpc; r0 < p.rows_pad; r0 += row_step) {
     const int64_t r = r0 + grp;
     const bool live = r < p.rows, stored = r < p.rows_pad;
     uint4 h[V];
@@ -195,18 +213,21 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
       uint16_t* ho = RES ? p.h + r * p.cols + 8 * lane : nullptr;
       const bool all = V * tpr == nv && live;                    // nothing to test per vector
       float2 q = make_float2(0.0f, 0.0f);
-      ptx::cp_async_wait<0>();
+      ptx::cp_async_wait<kAhead - 1>();
+      const uint4* s = slots + buf * (RES ? 2 : 1) * V * nt + tid;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        h[j] = slots[j * nt + tid];
+        h[j] = s[j * nt];
         if (RES) {
-          const uint4 e = slots[(V + j) * nt + tid];
+          const uint4 e = s[(V + j) * nt];
           h[j] = make_uint4(add_bf16x2(h[j].x, e.x), add_bf16x2(h[j].y, e.y),
                             add_bf16x2(h[j].z, e.z), add_bf16x2(h[j].w, e.w));
         }
       }
-      const int64_t next = r + int64_t(gridDim.x) * rpc;
-      if (next - grp < p.rows_pad) prefetch(next);
+      const int64_t next = r0 + kAhead * row_step;
+      if (next < p.rows_pad) prefetch(next + grp, buf);
+      else if (kAhead > 1) ptx::cp_async_commit();
+      if (kAhead > 1) buf = buf + 1 == kAhead ? 0 : buf + 1;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         if (RES && (all || (live && j * tpr + lane < nv)))
@@ -614,7 +635,10 @@ cudaError_t launch_rows(const NormParams& p, int* ctas, cudaStream_t st) {
               : pl.v == 2 ? norm_row_kernel<2, OUT, RES>
               : pl.v == 4 ? norm_row_kernel<4, OUT, RES>
                           : norm_row_kernel<8, OUT, RES>;
-  const size_t smem = size_t(RES ? 2 : 1) * pl.v * pl.block * 16;
+  const int ahead = pl.v == 1   ? rows_ahead<1, RES>()
+                    : pl.v == 2 ? rows_ahead<2, RES>()
+                                : 1;
+  const size_t smem = size_t(RES ? 2 : 1) * ahead * pl.v * pl.block * 16;
   if (smem > 47 * 1024) {                          // 48 KB with the static part
     static ContextOnce attr[2] = {};               // v = 4 and 8, 512 threads
     const cudaError_t e = once_per_context(attr[pl.v > 4], [&] {
