@@ -379,7 +379,9 @@ typedef struct {
   int64_t ldx, ldr;
   int64_t rows, cols;
   int32_t gamma_fp32;
-  float eps;             /* >= 0 and finite; with eps 0 a row of zeros gives NaN (0 * inf) */
+  float eps;             /* >= 0 and finite; with eps 0 a row of zeros gives NaN (0 * inf), and so
+                            does one so small (below 2^-75) that its squares vanish in fp32:
+                            infinities there */
 } fp8_norm_input;
 
 /* Bytes of scratch fp8_rmsnorm_quantize needs (0 for a NULL recipe: the bf16 output alone). */
