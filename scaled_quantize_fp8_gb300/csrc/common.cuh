@@ -268,7 +268,12 @@ __device__ __forceinline__ uint4 ldg_nc_v4_sched(const void* p) {
   return v;
 }
 
-// 16-byte store with an L2 cache policy.
+// 8- and 16-byte stores with an L2 cache policy.
+__device__ __forceinline__ void stg_v2_policy(void* p, uint2 v, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v2.u32 [%0], {%1,%2}, %3;" ::"l"(p), "r"(v.x), "r"(v.y),
+               "l"(policy)
+               : "memory");
+}
 __device__ __forceinline__ void stg_v4_policy(void* p, uint4 v, uint64_t policy) {
   asm volatile("st.global.L2::cache_hint.v4.u32 [%0], {%1,%2,%3,%4}, %5;" ::"l"(p), "r"(v.x),
                "r"(v.y), "r"(v.z), "r"(v.w), "l"(policy)

@@ -13,7 +13,7 @@
 // Both evaluate y with the same two roundings, so a value has the same y in either copy.
 //
 // Bound by memory: 8192 x 4096 with a residual and both MXFP8 copies has to move 271 MB, 39.9 us
-// at the 6780 GB/s of a copy; the two kernels take 52.2 (the row kernel alone 38.8, 0.90 of that
+// at the 6780 GB/s of a copy; the two kernels take 48.4 (the row kernel alone 37.7, 0.92 of that
 // rate). Why two: rstd needs a whole row, a column's scale 32 or 128 rows. One kernel that does
 // both in one pass (a cluster of CTAs with 32 or 128 whole rows in registers) took 55.7: its
 // loads, its exchange and its stores do not overlap, and no room is left to fetch the next rows
@@ -100,7 +100,7 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // is made twice, for the maxima and for the codes: kept in between, two vectors are no faster
 // (39.0 us either way) and four spill.
 //
-// What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 39.0 us, 6050
+// What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 37.7 us, 6260
 // GB/s); without one the instructions as much (19.4 us for 15.0 of memory; 32-bit offsets and sums
 // read four at a time gave 1.1 of the 20.5 before).
 
@@ -149,11 +149,15 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
   const int warp = (grp * tpr + lane) >> 5, wl = (grp * tpr + lane) & 31, nv = p.cols >> 3;
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
   const bool want_y = OUT != N_STATS || p.y != nullptr || p.part != nullptr;
-  // x and the residual are read once; h is read again by the column kernel (x without a
-  // residual), which then finds all but 1 % of its 67 MB in L2: 52.6 us for both, 55.7 with all
-  // of it marked to be evicted first
+  // x and the residual are read once; h (x without a residual) is read again by the column kernel,
+  // which then finds all but 1 % of its 67 MB in L2. With a residual the codes, not read before
+  // the kernel is over, go first too. 8192 x 4096, both copies: MXFP8 48.4 us, delayed 45.7; the
+  // codes as ordinary lines 49.8 and 48.2 (with a GEMM behind the norm 132.9 and 116.5, else 133.6
+  // and 121: it gains nothing from finding the codes in L2); h as ordinary lines 53.2 and 50.8.
+  // Without a residual there is room for them, and the GEMM does find them (118 us, else 120).
   const uint64_t first = ptx::l2_evict_first_policy(), last = ptx::l2_evict_last_policy();
   const uint64_t xpol = RES || !p.keep_h ? first : last, hpol = p.keep_h ? last : first;
+  const uint64_t codes = RES ? first : ptx::l2_evict_normal_policy();
   const int nt = tpr * rpc, tid = grp * tpr + lane;
   constexpr int kAhead = rows_ahead<V, RES>();
 
@@ -339,9 +343,10 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(y[k], s2);
         if (in && stored)
-          *reinterpret_cast<uint2*>(row + 8 * j * tpr) =
-              make_uint2(cvt_e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y),
-                         cvt_e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y));
+          stg_v2_policy(row + 8 * j * tpr,
+                        make_uint2(cvt_e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y),
+                                   cvt_e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y)),
+                        codes);
       }
     }
   }
@@ -407,7 +412,11 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
   const bool want_col = FULL || p.col != nullptr, col_bf16 = !FULL && p.col_bf16;
   pdl_wait();
 
-  const uint64_t policy = ptx::l2_evict_first_policy();          // the last read of h
+  // The last read of h. One that was just written becomes an ordinary line: evicted first, its
+  // write-back would meet the copies' (both MXFP8 copies, 8192 x 4096: 52.5 us, 49.9). x, which
+  // is not dirty, makes room for them (without a residual 33.4 us, as an ordinary line 34.5).
+  const uint64_t first = ptx::l2_evict_first_policy();
+  const uint64_t policy = p.res != nullptr ? ptx::l2_evict_normal_policy() : first;
   const auto prefetch = [&](int tile, int buf) {
     // thread t copies piece t % 8 of the rows t / 8, t / 8 + 16, ..
     const int64_t r0 = int64_t(tile) * 128, r = r0 + (t >> 3);
@@ -590,13 +599,15 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
       uint32_t at = uint32_t(c) * pitch + uint32_t(r);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        *reinterpret_cast<uint2*>(p.col + at) =
-            make_uint2(cvt_e4m3x4(y[0][k].x, y[1][k].x, y[2][k].x, y[3][k].x),
-                       cvt_e4m3x4(y[4][k].x, y[5][k].x, y[6][k].x, y[7][k].x));
+        stg_v2_policy(p.col + at,
+                      make_uint2(cvt_e4m3x4(y[0][k].x, y[1][k].x, y[2][k].x, y[3][k].x),
+                                 cvt_e4m3x4(y[4][k].x, y[5][k].x, y[6][k].x, y[7][k].x)),
+                      first);
         at += pitch;
-        *reinterpret_cast<uint2*>(p.col + at) =
-            make_uint2(cvt_e4m3x4(y[0][k].y, y[1][k].y, y[2][k].y, y[3][k].y),
-                       cvt_e4m3x4(y[4][k].y, y[5][k].y, y[6][k].y, y[7][k].y));
+        stg_v2_policy(p.col + at,
+                      make_uint2(cvt_e4m3x4(y[0][k].y, y[1][k].y, y[2][k].y, y[3][k].y),
+                                 cvt_e4m3x4(y[4][k].y, y[5][k].y, y[6][k].y, y[7][k].y)),
+                      first);
         at += pitch;
       }
     }
@@ -627,9 +638,9 @@ cudaError_t launch_rows(const NormParams& p, int* ctas, cudaStream_t st) {
   // as many CTAs as run at once: a quarter of an SM has registers for seven warps at 72 a thread,
   // six at 80, four at 128. One CTA too many per SM runs alone at the end (6528 x 5120, row copy:
   // 46 us instead of 40).
-  const int64_t grid =
-      std::min<int64_t>((p.rows_pad + rpc - 1) / rpc,
-                        int64_t(num_sms()) * std::max(1, (pl.v <= 2 ? 896 : pl.v == 4 ? 768 : 512) / pl.block));
+  const int per_sm = (pl.v <= 2 ? 896 : pl.v == 4 ? 768 : 512) / pl.block;
+  const int64_t grid = std::min<int64_t>((p.rows_pad + rpc - 1) / rpc,
+                                         int64_t(num_sms()) * std::max(1, per_sm));
   if (ctas != nullptr) *ctas = int(grid);
   auto kern = pl.v == 1   ? norm_row_kernel<1, OUT, RES>
               : pl.v == 2 ? norm_row_kernel<2, OUT, RES>
