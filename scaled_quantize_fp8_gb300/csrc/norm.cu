@@ -13,7 +13,7 @@
 // Both evaluate y with the same two roundings, so a value has the same y in either copy.
 //
 // Bound by memory: 8192 x 4096 with a residual and both MXFP8 copies has to move 271 MB, 39.9 us
-// at the 6780 GB/s of a copy; the two kernels take 48.4 (the row kernel alone 37.7, 0.92 of that
+// at the 6780 GB/s of a copy; the two kernels take 48.7 (the row kernel alone 37.7, 0.92 of that
 // rate). Why two: rstd needs a whole row, a column's scale 32 or 128 rows. One kernel that does
 // both in one pass (a cluster of CTAs with 32 or 128 whole rows in registers) took 55.7: its
 // loads, its exchange and its stores do not overlap, and no room is left to fetch the next rows
@@ -98,7 +98,7 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // the next row to shared memory (cp.async) while it works on the present one, and gamma stays in
 // registers. Sums of squares in fp32, two a thread, then over lanes and warps in a fixed order. y
 // is made twice, for the maxima and for the codes: kept in between, two vectors are no faster
-// (39.0 us either way) and four spill.
+// (39.0 us either way, measured at that time) and four spill.
 //
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 37.7 us, 6260
 // GB/s); without one the instructions as much (19.4 us for 15.0 of memory; 32-bit offsets and sums
@@ -151,9 +151,9 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
   const bool want_y = OUT != N_STATS || p.y != nullptr || p.part != nullptr;
   // x and the residual are read once; h (x without a residual) is read again by the column kernel,
   // which then finds all but 1 % of its 67 MB in L2. With a residual the codes, not read before
-  // the kernel is over, go first too. 8192 x 4096, both copies: MXFP8 48.4 us, delayed 45.7; the
-  // codes as ordinary lines 49.8 and 48.2 (with a GEMM behind the norm 132.9 and 116.5, else 133.6
-  // and 121: it gains nothing from finding the codes in L2); h as ordinary lines 53.2 and 50.8.
+  // the kernel is over, go first too. 8192 x 4096, both copies: MXFP8 48.7 us, delayed 46.1; the
+  // codes as ordinary lines 49.4 and 47.8 (with a GEMM behind the norm 132.9 and 116.5, else 133.6
+  // and 121: it gains nothing from finding the codes in L2); h as ordinary lines 52.0 and 49.0.
   // Without a residual there is room for them, and the GEMM does find them (118 us, else 120).
   const uint64_t first = ptx::l2_evict_first_policy(), last = ptx::l2_evict_last_policy();
   const uint64_t xpol = RES || !p.keep_h ? first : last, hpol = p.keep_h ? last : first;
@@ -379,14 +379,14 @@ __global__ void __launch_bounds__(512) norm_amax_kernel(const uint32_t* part, in
 // one to the other buffer in shared memory (cp.async); the 16-byte pieces of row r are exchanged
 // by (r / 8) % 8 so that the rows eight apart that lanes read at once lie in different banks.
 //
-// 13.4 us at 8192 x 4096 (MXFP8), where its 35 MB of stores alone would take 5. No one resource
-// bounds it: L1, the ALUs and the schedulers are each about half busy; without its loads it takes
-// 3 us less, without its stores 4 less. Loads by TMA, two tiles ahead, column lines put together
-// in shared memory, a warp's rows one below the other: all within 0.5 us.
+// 10.9 us at 8192 x 4096 (MXFP8), where its 35 MB of stores alone would take 5. No one resource
+// bounds it: L1, the ALUs and the schedulers are each about half busy; without its loads it took
+// 3 us less, without its stores 4 less. Loads by TMA, two and three tiles ahead, column lines put
+// together in shared memory, a warp's rows one below the other: all within 0.5 us.
 //
-// CTAs per SM: five, at 102 registers a thread (MXFP8: 52.6 us for both copies; four 52.9, six,
-// which spill, 54.6), but six where there are no maxima (FULL, per-tensor scales: 49.5; five
-// 50.0).
+// CTAs per SM: five, at 102 registers a thread (MXFP8: 48.7 us for both copies; four 49.2, six,
+// which spill, 52.5), but six where there are no maxima (FULL, per-tensor scales: 46.1; five
+// 46.4).
 template <int OUT, bool FULL>
 constexpr int col_ctas() {
   return OUT == N_TENSOR && FULL ? 6 : 5;
@@ -399,7 +399,7 @@ struct NormColSmem {
 };
 
 // FULL: nothing but the FP8 column copy is wanted and every tile lies inside the padded tensor,
-// so nothing is tested per row (8192 x 4096, both copies: 52.6 us, else 55.4, with a few spills).
+// so nothing is tested per row (8192 x 4096, both copies: 48.7 us, else 52.6, with a few spills).
 template <int OUT, bool FULL>
 __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
     norm_col_kernel(const __grid_constant__ NormParams p, const int tiles_c, const int tiles_r) {
@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
   pdl_wait();
 
   // The last read of h. One that was just written becomes an ordinary line: evicted first, its
-  // write-back would meet the copies' (both MXFP8 copies, 8192 x 4096: 52.5 us, 49.9). x, which
-  // is not dirty, makes room for them (without a residual 33.4 us, as an ordinary line 34.5).
+  // write-back would meet the copies' (both MXFP8 copies, 8192 x 4096: 52.5 us, 48.7). x, which
+  // is not dirty, makes room for them (without a residual 32.9 us, as an ordinary line 34.1).
   const uint64_t first = ptx::l2_evict_first_policy();
   const uint64_t policy = p.res != nullptr ? ptx::l2_evict_normal_policy() : first;
   const auto prefetch = [&](int tile, int buf) {
@@ -624,9 +624,9 @@ constexpr int kNormMaxParts = 4096;   // amax partials: one per CTA of the row k
 // Vectors a thread. One row per SM or less: one, as the row's latency counts (64 x 4096, MXFP8 row
 // copy: 2.0 us; two 2.2, four 3.0). Rows to stream: enough loads in flight, but no more registers
 // than that needs. With a residual (twice the loads) two, 4096 columns then being 256 threads
-// (8192 x 4096, both copies: 52.5 us; four 53.8, one 87.3); without one four (34.4; two 44.4); and
-// four for longer rows, of which two would make CTAs of 512 threads, one per SM
-// (4096 x 8192, row copy: 40.3; two 43.2).
+// (8192 x 4096, row copy: 37.7 us; four 39.2, one 47.1); without one four (both copies: 32.9; two
+// 36.9); and four for longer rows, of which two would make CTAs of 512 threads, one per SM
+// (4096 x 8192, row copy: 38.0; two 42.2).
 RowPlan fwd_plan(int64_t rows, int cols, bool res) {
   return row_plan(cols, rows <= num_sms() ? 1 : res && cols <= 4096 ? 2 : 4, 256);
 }
