@@ -409,6 +409,8 @@ size_t fp8_rmsnorm_workspace_bytes(const fp8_recipe *recipe, int64_t rows, int64
  *   workspace  fp8_rmsnorm_workspace_bytes() of device scratch.
  *   dev_status is not written: nothing in these kernels waits for anything that could fail to
  *              come. The same holds for fp8_rmsnorm_bwd.
+ * A row's h, rstd, y and row copy do not depend on the other rows nor on their number (per-tensor
+ * scales aside).
  * NaN in y gives code 0x7F. A NaN in a row of h makes the whole row NaN. An infinity, or squares
  * whose sum leaves fp32's range (|h| of 2^63 and more), make the row's rstd 0: its finite elements
  * become zeros, the infinite ones NaN. Apart from h no output may overlap an input.

@@ -142,7 +142,10 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     norm_row_kernel(const __grid_constant__ NormParams p) {
   constexpr bool kGammaRegs = V <= 4;               // eight vectors: gamma comes from L1
   pdl_wait();
-  __shared__ alignas(16) float red[2][16];
+  // Sums of a row's squares: with four vectors, the first and third apart from the second and
+  // fourth, so that the order of additions is that of two vectors and twice the threads.
+  constexpr int kSums = V == 4 ? 2 : 1;
+  __shared__ alignas(16) float red[2][16 * kSums];
   __shared__ uint32_t redm[16];
   extern __shared__ uint4 slots[];                  // each thread's next rows
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
@@ -212,11 +215,13 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     const int64_t r = r0 + grp;
     const bool live = r < p.rows, stored = r < p.rows_pad;
     uint4 h[V];
-    float ss;
+    float ss[kSums];
     {
       uint16_t* ho = RES ? p.h + r * p.cols + 8 * lane : nullptr;
       const bool all = V * tpr == nv && live;                    // nothing to test per vector
-      float2 q = make_float2(0.0f, 0.0f);
+      float2 q[kSums];
+#pragma unroll
+      for (int k = 0; k < kSums; ++k) q[k] = make_float2(0.0f, 0.0f);
       ptx::cp_async_wait<kAhead - 1>();
       const uint4* s = slots + buf * (RES ? 2 : 1) * V * nt + tid;
 #pragma unroll
@@ -240,30 +245,40 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = make_float2(bf16_lo(w[k]), bf16_hi(w[k]));
-          q = __ffma2_rn(f, f, q);
+          q[j % kSums] = __ffma2_rn(f, f, q[j % kSums]);
         }
       }
-      ss = q.x + q.y;
-    }
-    if (warps != 0) ss += __shfl_xor_sync(0xffffffffu, ss, 16);
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      for (int k = 0; k < kSums; ++k) ss[k] = q[k].x + q[k].y;
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSums; ++k) {
+      if (warps != 0) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], 16);
+#pragma unroll
+      for (int o = 8; o > 0; o >>= 1) ss[k] += __shfl_xor_sync(0xffffffffu, ss[k], o);
+      sum += ss[k];
+    }
     if (warps > 1) {
-      if ((lane & 31) == 0) red[phase][warp] = ss;
+      const int n = kSums * warps;
+      float* q = red[phase] + grp * n;
+      if ((lane & 31) == 0) {
+#pragma unroll
+        for (int k = 0; k < kSums; ++k) q[k * warps + (lane >> 5)] = ss[k];
+      }
       __syncthreads();
-      const float* q = red[phase] + grp * warps;
-      ss = 0.0f;
-      if ((warps & 3) == 0) {
-        for (int i = 0; i < warps; i += 4) {
+      sum = 0.0f;
+      if ((n & 3) == 0) {
+        for (int i = 0; i < n; i += 4) {
           const float4 a = *reinterpret_cast<const float4*>(q + i);
-          ss += (a.x + a.y) + (a.z + a.w);
+          sum += (a.x + a.y) + (a.z + a.w);
         }
       } else {
-        for (int i = 0; i < warps; ++i) ss += q[i];
+        for (int i = 0; i < n; ++i) sum += q[i];
       }
       phase ^= 1;               // the next row's sums go to the other buffer: one barrier a row
     }
-    const float rstd = rsqrtf(fmaf(ss, p.inv_cols, p.eps));
+    const float rstd = rsqrtf(fmaf(sum, p.inv_cols, p.eps));
     if (live && lane == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
     if (!want_y) continue;
     const float rl = live ? rstd : 0.0f;                         // padding rows: (0 0) gamma = 0
@@ -621,19 +636,22 @@ namespace {
 
 constexpr int kNormMaxParts = 4096;   // amax partials: one per CTA of the row kernel
 
-// Vectors a thread. One row per SM or less: one, as the row's latency counts (64 x 4096, MXFP8 row
-// copy: 2.0 us; two 2.2, four 3.0). Rows to stream: enough loads in flight, but no more registers
-// than that needs. With a residual (twice the loads) two, 4096 columns then being 256 threads
-// (8192 x 4096, row copy: 37.7 us; four 39.2, one 47.1); without one four (both copies: 32.9; two
-// 36.9); and four for longer rows, of which two would make CTAs of 512 threads, one per SM
-// (4096 x 8192, row copy: 38.0; two 42.2).
-RowPlan fwd_plan(int64_t rows, int cols, bool res) {
-  return row_plan(cols, rows <= num_sms() ? 1 : res && cols <= 4096 ? 2 : 4, 256);
+// Vectors a thread: enough loads in flight, but no more registers than that needs. With a residual
+// (twice the loads) two, 4096 columns then being 256 threads (8192 x 4096, row copy: 37.7 us; four
+// 39.2, one 47.1); without one four (both copies: 32.9; two 36.9); and four for longer rows, of
+// which two would make CTAs of 512 threads, one per SM (4096 x 8192, row copy: 38.0; two 42.2).
+// A row's sum, and so its last bit, must not depend on how many rows there are (a token served
+// alone gives what it gives in a batch) nor on whether the residual was added here: the threads
+// are twice as many with two vectors, which are used only where that comes out even, and few rows,
+// which one vector would do sooner (64 x 4096: 2.0 us; two 2.2, four 3.0), are no exception.
+RowPlan fwd_plan(int cols, bool res) {
+  const RowPlan two = row_plan(cols, 2, 256), four = row_plan(cols, 4, 256);
+  return res && cols <= 4096 && two.tpr == 2 * four.tpr ? two : four;
 }
 
 template <int OUT, bool RES>
 cudaError_t launch_rows(const NormParams& p, int* ctas, cudaStream_t st) {
-  const RowPlan pl = fwd_plan(p.rows_pad, p.cols, RES);
+  const RowPlan pl = fwd_plan(p.cols, RES);
   const int rpc = pl.block / pl.tpr;
   // as many CTAs as run at once: a quarter of an SM has registers for seven warps at 72 a thread,
   // six at 80, four at 128. One CTA too many per SM runs alone at the end (6528 x 5120, row copy:

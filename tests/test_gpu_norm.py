@@ -503,3 +503,26 @@ def test_more_rows_than_sms(kind, rows, cols, residual):
 def test_backward_of_many_rows(rows, cols):
     check_bwd(rows, cols)
     check_bwd(rows, cols, dres=False, gamma_fp32=True)
+
+
+@pytest.mark.parametrize("cols", [128, 512, 640, 1024, 2176, 2560, 4096, 5120, 16384])
+@pytest.mark.parametrize("residual", [False, True])
+def test_rows_do_not_depend_on_their_number(cols, residual):
+    """A row alone, in a small and in a large batch, and with the residual added before: the same
+    bits."""
+    rec = F.Recipe(kind="mxfp8")
+    x = to_dev_bf16(bf16_bits_normal(700, cols, seed=1))
+    res = to_dev_bf16(bf16_bits_normal(700, cols, seed=2)) if residual else None
+    g = _dev_gamma(_gamma(cols), False)
+
+    def run(a, b):
+        r = None if res is None else res[a:b]
+        q, h, rstd, _ = F.rmsnorm_quantize(rec, x[a:b], g, residual=r, want_col=False)
+        return q.row[:b - a], h, rstd
+
+    ref = run(0, 700)
+    for a, b in ((0, 1), (5, 6), (699, 700), (100, 140), (300, 600)):
+        for got, want in zip(run(a, b), ref):
+            assert torch.equal(got, want[a:b])
+    q, _, rstd, _ = F.rmsnorm_quantize(rec, ref[1], g, want_col=False)
+    assert torch.equal(q.row[:700], ref[0]) and torch.equal(rstd, ref[2])
