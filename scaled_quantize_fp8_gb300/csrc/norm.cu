@@ -101,8 +101,8 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // (39.0 us either way, measured at that time) and four spill.
 //
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 37.7 us, 6260
-// GB/s); without one the instructions as much (19.4 us for 15.0 of memory; 32-bit offsets and sums
-// read four at a time gave 1.1 of the 20.5 before).
+// GB/s); without one the instructions as much (20.6 us for 15.0 of memory, of which the second sum
+// over the lanes, see there, is 1.2).
 
 // Reduce the V vectors' values over the lanes that differ in the bits OFF .. 1: as long as there
 // is more than one vector, a lane passes on half of them and keeps the half that its bit names.
@@ -143,7 +143,8 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
   constexpr bool kGammaRegs = V <= 4;               // eight vectors: gamma comes from L1
   pdl_wait();
   // Sums of a row's squares: with four vectors, the first and third apart from the second and
-  // fourth, so that the order of additions is that of two vectors and twice the threads.
+  // fourth, so that the order of additions is that of two vectors and twice the threads. (Only
+  // where the row is short enough to get two: a branch that costs more than it saves.)
   constexpr int kSums = V == 4 ? 2 : 1;
   __shared__ alignas(16) float red[2][16 * kSums];
   __shared__ uint32_t redm[16];
@@ -638,7 +639,7 @@ constexpr int kNormMaxParts = 4096;   // amax partials: one per CTA of the row k
 
 // Vectors a thread: enough loads in flight, but no more registers than that needs. With a residual
 // (twice the loads) two, 4096 columns then being 256 threads (8192 x 4096, row copy: 37.7 us; four
-// 39.2, one 47.1); without one four (both copies: 32.9; two 36.9); and four for longer rows, of
+// 39.2, one 47.1); without one four (both copies: 33.6; two 36.9); and four for longer rows, of
 // which two would make CTAs of 512 threads, one per SM (4096 x 8192, row copy: 38.0; two 42.2).
 // A row's sum, and so its last bit, must not depend on how many rows there are (a token served
 // alone gives what it gives in a batch) nor on whether the residual was added here: the threads
