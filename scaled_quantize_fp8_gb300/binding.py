@@ -436,6 +436,39 @@ def _gamma(gamma: torch.Tensor, cols: int):
     return 1 if dtype is _FP32 else 0
 
 
+def _check_copy(codes, scale, shape, size, block):
+    """A copy's buffers before the kernels write it: codes of `size` bytes in the copy's shape, and
+    for block scales as many bytes as they take, one for 32 codes (four for 128 come to the same).
+    Returns whether they lie on the GPU."""
+    if codes is None or codes.shape != shape or codes.itemsize != size \
+            or not codes.is_contiguous():
+        raise ValueError(f"out: contiguous copies of shape {shape} with {size} bytes an element")
+    if not block or scale is None:                 # (the library refuses scales that are missing)
+        return codes.is_cuda
+    if scale.nbytes < shape[0] * shape[1] // 32 or not scale.is_contiguous():
+        raise ValueError(f"out: contiguous scales of a copy of shape {shape}")
+    return codes.is_cuda and scale.is_cuda
+
+
+def _check_out(out: QTensor, recipe: Recipe, rows, cols, want_row, want_col):
+    """The buffers of a caller's `out`: as empty_qtensor makes them for an activation of `rows`
+    padded rows under this recipe. Returns whether they lie on the GPU."""
+    block = recipe.kind in ("mxfp8", "blockwise")
+    on_gpu = True
+    if want_row:
+        on_gpu = _check_copy(out.row, out.row_scale, (rows, cols), 1, block)
+    if want_col:                                   # without FP8 wgrad in bf16, and no scales
+        fp8 = recipe.fp8_wgrad
+        on_gpu &= _check_copy(out.col, out.col_scale, (cols, rows), 1 if fp8 else 2, block and fp8)
+    if not block:
+        for t in (out.amax, out.scale, out.scale_inv):
+            if t is not None:
+                if t.dtype is not _FP32 or t.numel() == 0:
+                    raise ValueError("out: fp32 amax, scale and scale_inv")
+                on_gpu &= t.is_cuda
+    return on_gpu
+
+
 def rmsnorm_workspace_bytes(recipe: Recipe, rows, cols):
     rc = recipe.c()
     return int(L.load().fp8_rmsnorm_workspace_bytes(ctypes.byref(rc), rows, cols))
@@ -483,6 +516,7 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
     inp = L.pack_norm_input(x.data_ptr(), res_ptr, gamma.data_ptr(), ldx, ldr, rows, cols,
                             _gamma(gamma, cols), eps)
     rc = out_ref = None
+    on_gpu = True
     if want_row or want_col:
         q = 128 if recipe.kind in ("mxfp8", "blockwise") else 16
         padded = -(-rows // q) * q
@@ -490,12 +524,11 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
             with torch.cuda.stream(stream):
                 out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
                                     device=x.device)
-        elif (want_row and (out.row is None or out.row.shape != (padded, cols))) or \
-                (want_col and (out.col is None or out.col.shape != (cols, padded))):
-            raise ValueError(f"out: copies of {padded} rows (padded) and {cols} columns")
+        else:
+            on_gpu = _check_out(out, recipe, padded, cols, want_row, want_col)
         ct = out.c()
         out_ref, rc = ctypes.byref(ct), ctypes.byref(recipe.c())
-    if not (x.is_cuda and gamma.is_cuda and h.is_cuda and rstd.is_cuda
+    if not (on_gpu and x.is_cuda and gamma.is_cuda and h.is_cuda and rstd.is_cuda
             and (residual is None or residual.is_cuda) and (y is None or y.is_cuda)
             and (workspace is None or workspace.is_cuda)):
         _not_on_gpu()

@@ -1,0 +1,92 @@
+"""What the Python binding checks before the library sees an address, on CPU tensors: a call that
+passes every check of shapes and types ends in the TypeError for tensors that are not on the GPU."""
+import pytest
+import torch
+
+from scaled_quantize_fp8_gb300 import binding
+from scaled_quantize_fp8_gb300 import build as B
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    B.build()
+
+
+KINDS = ["mxfp8", "blockwise", "tensorwise", "delayed"]
+
+
+def _call(rec, out, rows=5, cols=256, **kw):
+    x = torch.zeros(rows, cols, dtype=torch.bfloat16)
+    return binding.rmsnorm_quantize(rec, x, torch.zeros(cols), out=out, **kw)
+
+
+def _out(rec, cols=256, role="activation"):
+    rows = 128 if rec.kind in ("mxfp8", "blockwise") else 16
+    return binding.empty_qtensor(rec, rows, cols, role, device="cpu")
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_norm_refuses_a_column_copy_of_the_other_type(kind):
+    """Without FP8 wgrad the column copy takes two bytes an element, else one: buffers kept from
+    before the recipe's flag changed have the right shape and the wrong size."""
+    rec = binding.Recipe(kind=kind)
+    out = _out(rec)
+    rec.fp8_wgrad = False
+    with pytest.raises(ValueError):
+        _call(rec, out)
+    out = _out(rec)
+    rec.fp8_wgrad = True
+    with pytest.raises(ValueError):
+        _call(rec, out)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("name", ["row", "col"])
+def test_norm_refuses_copies_that_do_not_lie_row_by_row(kind, name):
+    rec = binding.Recipe(kind=kind)
+    out = _out(rec)
+    t = getattr(out, name)
+    setattr(out, name, t.t().contiguous().t())
+    with pytest.raises(ValueError):
+        _call(rec, out)
+    setattr(out, name, t[:1].expand(t.shape))
+    with pytest.raises(ValueError):
+        _call(rec, out)
+
+
+@pytest.mark.parametrize("kind", ["mxfp8", "blockwise"])
+@pytest.mark.parametrize("name", ["row_scale", "col_scale"])
+def test_norm_refuses_scales_that_are_too_few(kind, name):
+    rec = binding.Recipe(kind=kind)
+    out = _out(rec)
+    t = getattr(out, name)
+    setattr(out, name, t.reshape(-1)[:-1])
+    with pytest.raises(ValueError):
+        _call(rec, out)
+    setattr(out, name, t.reshape(-1)[:1].expand(t.numel()))
+    with pytest.raises(ValueError):
+        _call(rec, out)
+    if kind == "blockwise":                         # one scale for 128 x 128, as weights have
+        with pytest.raises(ValueError):
+            _call(rec, _out(rec, role="weight"))
+
+
+@pytest.mark.parametrize("kind", ["tensorwise", "delayed"])
+@pytest.mark.parametrize("name", ["amax", "scale", "scale_inv"])
+def test_norm_refuses_malformed_scalars(kind, name):
+    rec = binding.Recipe(kind=kind)
+    for bad in (torch.zeros(0), torch.zeros(1, dtype=torch.bfloat16)):
+        out = _out(rec)
+        setattr(out, name, bad)
+        with pytest.raises(ValueError):
+            _call(rec, out)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("wgrad", [True, False])
+def test_norm_takes_what_empty_qtensor_makes(kind, wgrad):
+    rec = binding.Recipe(kind=kind, fp8_wgrad=wgrad)
+    with pytest.raises(TypeError, match="CUDA"):    # nothing else is wrong with the call
+        _call(rec, _out(rec))
+    with pytest.raises(TypeError, match="CUDA"):
+        _call(rec, _out(rec), want_col=False)
