@@ -632,9 +632,11 @@ class GradList:
     tensors of any shape, dense in memory, on one device. `outs` are the tensors that
     grad_clip writes (the gradients themselves when not given), with the gradients' shapes and
     strides. The list holds the tensors' addresses: it is made once for gradients that stay in
-    place, and anew for new tensors. It also holds the results of grad_norm, `norm` and `coef`."""
+    place, and anew for new tensors. It also holds the results of grad_norm, `norm` and `coef`,
+    which come from the pool of `stream` (the current one if not given): a list whose calls run on
+    another stream is made for that one, or its making is waited for there."""
 
-    def __init__(self, grads, outs=None):
+    def __init__(self, grads, outs=None, stream=None):
         self.grads = list(grads)
         self.outs = self.grads if outs is None else list(outs)
         if len(self.outs) != len(self.grads):
@@ -650,7 +652,7 @@ class GradList:
         self.pointer = ctypes.pointer(self.items[0])
         self.on_gpu = all(t.is_cuda for t in self.grads + self.outs)
         self.device = self.grads[0].device if self.grads else torch.device("cuda")
-        self.norm, self.coef = torch.empty((2, 1), dtype=_FP32, device=self.device).unbind(0)
+        self.norm, self.coef = _empty((2, 1), _FP32, self.device, stream).unbind(0)
 
     def __len__(self):
         return len(self.grads)
@@ -675,7 +677,7 @@ def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tens
     small list)."""
     lib = L.load()
     if not isinstance(grads, GradList):
-        grads = GradList(grads)
+        grads = GradList(grads, stream=stream)
     n = len(grads.grads)
     norm = grads.norm if norm is None else _scalar(norm, "norm")
     coef = grads.coef if coef is None else _scalar(coef, "coef")
@@ -696,7 +698,7 @@ def grad_norm(grads, max_norm=float("inf"), scale=1.0, norm: Optional[torch.Tens
 def grad_clip(grads, coef: torch.Tensor, stream=None):
     """fp8_grad_clip: outs = grads * coef (coef as grad_norm returns it). Returns the outs."""
     if not isinstance(grads, GradList):
-        grads = GradList(grads)
+        grads = GradList(grads, stream=stream)
     _scalar(coef, "coef")
     if not (grads.on_gpu and coef.is_cuda):
         _not_on_gpu()

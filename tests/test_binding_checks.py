@@ -90,3 +90,21 @@ def test_norm_takes_what_empty_qtensor_makes(kind, wgrad):
         _call(rec, _out(rec))
     with pytest.raises(TypeError, match="CUDA"):
         _call(rec, _out(rec), want_col=False)
+
+
+def test_results_of_a_plain_list_come_from_the_calls_stream(monkeypatch):
+    """grad_norm makes its own two results for a plain list of tensors. Taken from the current
+    stream's pool, they could be memory that work queued there still uses, or uses again, while
+    the kernels write them on the stream that was given."""
+    seen = []
+
+    def empty(shape, dtype, device, stream):
+        seen.append(stream)
+        return torch.empty(shape, dtype=dtype, device=device)
+
+    monkeypatch.setattr(binding, "_empty", empty)
+    with pytest.raises(TypeError, match="CUDA"):
+        binding.grad_norm([torch.ones(3)], stream="side")
+    assert seen == ["side"]
+    binding.GradList([torch.ones(3)], stream="other")
+    assert seen == ["side", "other"]
