@@ -641,8 +641,11 @@ class GradList:
         self.outs = self.grads if outs is None else list(outs)
         if len(self.outs) != len(self.grads):
             raise ValueError("outs: one tensor per gradient")
+        self.device = self.grads[0].device if self.grads else torch.device("cuda")
         self.items = (L.GradItem * max(1, len(self.grads)))()
         for i, (g, o) in enumerate(zip(self.grads, self.outs)):
+            if g.device != self.device or o.device != self.device:
+                raise ValueError("gradients and outs must lie on one device")
             if g.dtype not in _GRAD_DTYPES or o.dtype not in _GRAD_DTYPES:
                 raise TypeError("gradients: bf16 or fp32")
             if not _dense(g) or o.shape != g.shape or (o is not g and o.stride() != g.stride()):
@@ -650,8 +653,7 @@ class GradList:
             self.items[i] = L.GradItem(g.data_ptr(), o.data_ptr(), g.numel(),
                                        _GRAD_DTYPES[g.dtype], _GRAD_DTYPES[o.dtype])
         self.pointer = ctypes.pointer(self.items[0])
-        self.on_gpu = all(t.is_cuda for t in self.grads + self.outs)
-        self.device = self.grads[0].device if self.grads else torch.device("cuda")
+        self.on_gpu = not self.grads or self.device.type == "cuda"
         self.norm, self.coef = _empty((2, 1), _FP32, self.device, stream).unbind(0)
 
     def __len__(self):

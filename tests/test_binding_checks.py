@@ -108,3 +108,11 @@ def test_results_of_a_plain_list_come_from_the_calls_stream(monkeypatch):
     assert seen == ["side"]
     binding.GradList([torch.ones(3)], stream="other")
     assert seen == ["side", "other"]
+
+
+def test_gradients_on_more_than_one_device_are_refused():
+    """The kernels run on one GPU: an address of another device's memory is not theirs to read."""
+    here, there = torch.ones(3), torch.ones(3, device="meta")
+    for grads, outs in (([here, there], None), ([here], [there]), ([there, here], None)):
+        with pytest.raises(ValueError, match="device"):
+            binding.GradList(grads, outs)
