@@ -69,8 +69,9 @@ class NormGrad(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("gamma_fp32", ctypes.c_int32)]
 
 
-# The same two, and the clip rule, as bytes: the binding builds one per call, which takes half the
-# time of a Structure. The functions take either (their argument is a c_void_p).
+# The same two, the clip rule and the norm's recipe as bytes: the binding builds one per call, which
+# takes half the time of a Structure. The functions take either (their argument is a c_void_p).
+pack_recipe = struct.Struct("@iiiiiii").pack
 pack_norm_input = struct.Struct("@PPPqqqqif").pack
 pack_norm_grad = struct.Struct("@PPPPPqqqqqi4x").pack
 pack_clip_rule = struct.Struct("@ff").pack
@@ -124,8 +125,8 @@ _SIG = {
                                       ctypes.POINTER(Tensor), _P, _P]),
     "fp8_quantize_static_scratch": (_I32, [ctypes.POINTER(Recipe), _P, _I64, _I64, _I32, _I32,
                                            _I32, ctypes.POINTER(Tensor), _P, _P]),
-    "fp8_rmsnorm_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Recipe), _I64, _I64]),
-    "fp8_rmsnorm_quantize": (_I32, [ctypes.POINTER(Recipe), _P, _I32, _I32,
+    "fp8_rmsnorm_workspace_bytes": (ctypes.c_size_t, [_P, _I64, _I64]),
+    "fp8_rmsnorm_quantize": (_I32, [_P, _P, _I32, _I32,
                                     _P, _P, _P, ctypes.POINTER(Tensor), _P, ctypes.c_size_t, _P,
                                     _P]),
     "fp8_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),

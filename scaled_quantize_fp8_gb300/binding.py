@@ -30,19 +30,14 @@ class Recipe:
     fp8_wgrad: bool = True
     power_2_scales: bool = False
 
-    def c(self):
-        """The library's form; kept until a field changes."""
-        kept = self.__dict__.get("_c")
-        if kept is None:
-            kept = L.Recipe(KINDS[self.kind], 0 if self.format == "e4m3" else 1, int(self.margin),
-                            int(self.amax_history_len), 0 if self.amax_compute_algo == "max" else 1,
-                            1 if self.fp8_wgrad else 0, 1 if self.power_2_scales else 0)
-            self.__dict__["_c"] = kept
-        return kept
+    def _fields(self):
+        """The fields of the library's form, in order."""
+        return (KINDS[self.kind], 0 if self.format == "e4m3" else 1, int(self.margin),
+                int(self.amax_history_len), 0 if self.amax_compute_algo == "max" else 1,
+                1 if self.fp8_wgrad else 0, 1 if self.power_2_scales else 0)
 
-    def __setattr__(self, name, value):
-        self.__dict__.pop("_c", None)
-        self.__dict__[name] = value
+    def c(self):
+        return L.Recipe(*self._fields())
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -527,7 +522,7 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
         else:
             on_gpu = _check_out(out, recipe, padded, cols, want_row, want_col)
         ct = out.c()
-        out_ref, rc = ctypes.byref(ct), ctypes.byref(recipe.c())
+        out_ref, rc = ctypes.byref(ct), L.pack_recipe(*recipe._fields())
     if not (on_gpu and x.is_cuda and gamma.is_cuda and h.is_cuda and rstd.is_cuda
             and (residual is None or residual.is_cuda) and (y is None or y.is_cuda)
             and (workspace is None or workspace.is_cuda)):

@@ -116,3 +116,22 @@ def test_gradients_on_more_than_one_device_are_refused():
     for grads, outs in (([here, there], None), ([here], [there]), ([there, here], None)):
         with pytest.raises(ValueError, match="device"):
             binding.GradList(grads, outs)
+
+
+def test_a_recipe_holds_its_fields_and_nothing_else():
+    """Calls leave no trace in a Recipe: it can be rebuilt from vars(), a field set through the
+    dictionary counts, and a C form belongs to its caller."""
+    rec = binding.Recipe(kind="mxfp8", margin=1)
+    before = dict(vars(rec))
+    c = rec.c()
+    assert vars(rec) == before and binding.Recipe(**vars(rec)) == rec
+    rec.__dict__.update(margin=5)
+    assert rec.c().margin == 5
+    c.margin = 7
+    assert rec.c().margin == 5
+
+
+def test_the_packed_recipe_is_the_structure():
+    rec = binding.Recipe(kind="blockwise", format="hybrid", margin=-3, amax_history_len=17,
+                         amax_compute_algo="most_recent", fp8_wgrad=False, power_2_scales=True)
+    assert binding.L.pack_recipe(*rec._fields()) == bytes(rec.c())
