@@ -396,8 +396,9 @@ def _empty(shape, dtype, device, stream):
 
 
 def _buffer(t: Optional[torch.Tensor]):
-    """A workspace as the library takes it: address and bytes."""
-    return (None, 0) if t is None else (t.data_ptr(), t.nbytes)
+    """A workspace as the library takes it: address and bytes (none where they do not lie in one
+    piece, as in an expanded tensor)."""
+    return (None, 0) if t is None or not t.is_contiguous() else (t.data_ptr(), t.nbytes)
 
 
 def _rows_2d(t: torch.Tensor, cols, name: str):

@@ -135,3 +135,12 @@ def test_the_packed_recipe_is_the_structure():
     rec = binding.Recipe(kind="blockwise", format="hybrid", margin=-3, amax_history_len=17,
                          amax_compute_algo="most_recent", fp8_wgrad=False, power_2_scales=True)
     assert binding.L.pack_recipe(*rec._fields()) == bytes(rec.c())
+
+
+def test_a_workspace_counts_for_the_memory_it_has():
+    """An expanded tensor's bytes are not there: as small as none, so the call makes its own."""
+    whole = torch.zeros(64, dtype=torch.uint8)
+    assert binding._buffer(whole) == (whole.data_ptr(), 64)
+    assert binding._buffer(torch.zeros(8, 4))[1] == 128
+    for t in (None, whole[:1].expand(1 << 20), whole.view(8, 8)[:, :4]):
+        assert binding._buffer(t) == (None, 0)
