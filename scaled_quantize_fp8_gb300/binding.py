@@ -623,11 +623,17 @@ def _dense(t: torch.Tensor):
     return True
 
 
+def _same_order(a: torch.Tensor, b: torch.Tensor):
+    """Whether two tensors of one shape hold their elements in the same order in memory."""
+    return a.stride() == b.stride() or a.numel() == 0 or all(
+        size == 1 or s == t for size, s, t in zip(a.shape, a.stride(), b.stride()))
+
+
 class GradList:
     """The gradients of a step as fp8_grad_norm and fp8_grad_clip take them: bf16 or fp32 CUDA
     tensors of any shape, dense in memory, on one device. `outs` are the tensors that
     grad_clip writes (the gradients themselves when not given), with the gradients' shapes and
-    strides. The list holds the tensors' addresses: it is made once for gradients that stay in
+    order in memory. The list holds the tensors' addresses: it is made once for gradients that stay in
     place, and anew for new tensors. It also holds the results of grad_norm, `norm` and `coef`,
     which come from the pool of `stream` (the current one if not given): a list whose calls run on
     another stream is made for that one, or its making is waited for there."""
@@ -644,8 +650,8 @@ class GradList:
                 raise ValueError("gradients and outs must lie on one device")
             if g.dtype not in _GRAD_DTYPES or o.dtype not in _GRAD_DTYPES:
                 raise TypeError("gradients: bf16 or fp32")
-            if not _dense(g) or o.shape != g.shape or (o is not g and o.stride() != g.stride()):
-                raise ValueError("gradients must be dense, and outs have their shapes and strides")
+            if not _dense(g) or o.shape != g.shape or (o is not g and not _same_order(o, g)):
+                raise ValueError("gradients must be dense, and outs have their shapes and orders")
             self.items[i] = L.GradItem(g.data_ptr(), o.data_ptr(), g.numel(),
                                        _GRAD_DTYPES[g.dtype], _GRAD_DTYPES[o.dtype])
         self.pointer = ctypes.pointer(self.items[0])

@@ -144,3 +144,14 @@ def test_a_workspace_counts_for_the_memory_it_has():
     assert binding._buffer(torch.zeros(8, 4))[1] == 128
     for t in (None, whole[:1].expand(1 << 20), whole.view(8, 8)[:, :4]):
         assert binding._buffer(t) == (None, 0)
+
+
+def test_outs_need_the_gradients_order_not_their_strides():
+    """The stride of a dimension of one element says nothing about where elements lie."""
+    column = torch.zeros(5, 1)
+    for g, o in ((column.t(), torch.zeros(1, 5)), (torch.zeros(1, 5), column.t()),
+                 (torch.zeros(3, 0).t(), torch.zeros(0, 3))):
+        assert g.stride() != o.stride()
+        binding.GradList([g], [o])
+    with pytest.raises(ValueError):
+        binding.GradList([torch.zeros(2, 5)], [torch.zeros(5, 2).t()])
