@@ -1,9 +1,13 @@
 """Edges of the norm around the FP8 linear layer: buffers that a caller keeps, padding rows, ranges
 of values, and shapes whose groups of threads walk several rows."""
+import numpy as np
 import pytest
 import torch
 
-from helpers import cuda_ok
+from helpers import cuda_ok, from_dev_bf16, to_dev_bf16
+from oracle import fp8_oracle as O
+from test_gpu_norm import check_copies
+from workloads import bf16_bits_from_f32, bf16_bits_normal
 
 pytestmark = pytest.mark.gpu
 
@@ -24,3 +28,32 @@ def test_refuses_an_output_that_is_not_on_the_gpu(kind):
             setattr(out, name, getattr(out, name).cpu())
             with pytest.raises(TypeError):
                 F.rmsnorm_quantize(rec, x, torch.ones(256, device="cuda"), out=out)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("wgrad", [True, False])
+@pytest.mark.parametrize("rows,cols,residual", [(1, 256, True), (5, 128, False),
+                                                (125, 4096, False), (131, 640, True),
+                                                (1003, 2048, False), (300, 16384, True)])
+def test_padding_is_what_quantising_zero_rows_gives(kind, wgrad, rows, cols, residual):
+    """A gamma with negative and zero entries: products with a padding row's zeros have gamma's
+    sign, its codes (and bf16 columns) are +0 all the same. Rows that exist keep their -0."""
+    g = np.random.default_rng(3).standard_normal(cols).astype(np.float32)
+    g[::7], g[3::11] = 0.0, -0.0
+    rec = F.Recipe(kind=kind, fp8_wgrad=wgrad)
+    padded = -(-rows // ROW_Q[kind]) * ROW_Q[kind]
+    q = F.empty_qtensor(rec, padded, cols, "activation")
+    for t in (q.row, q.col):
+        t.fill_(0xA5)
+    x = bf16_bits_normal(rows, cols, seed=4)
+    x[:, ::5] = 0x8000
+    res = to_dev_bf16(np.full_like(x, 0x8000)) if residual else None
+    q, h, rstd, _ = F.rmsnorm_quantize(rec, to_dev_bf16(x), torch.from_numpy(g).cuda(),
+                                       residual=res, out=q)
+    torch.cuda.synchronize()
+    y = O.rmsnorm_y_f32(from_dev_bf16(h), rstd.cpu().numpy(), g)
+    check_copies(q, y, kind, scale=1.0, col=wgrad)
+    if not wgrad:
+        yp = np.zeros((padded, cols), dtype=np.float32)
+        yp[:rows] = y
+        assert np.array_equal(from_dev_bf16(q.col), bf16_bits_from_f32(np.ascontiguousarray(yp.T)))
