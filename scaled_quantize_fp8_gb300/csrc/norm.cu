@@ -341,7 +341,9 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
       const int v = j * tpr + lane;
       const bool in = v < nv;                 // uniform over the lanes of a block
       float2 y[4];
-      norm_row8(h[j], rl, gamma_of(j), y);
+      // (for the amax, no NaN where a row's rstd is infinite and a lane has no column)
+      const float rj = OUT == N_STATS || OUT == N_TENSOR ? (in ? rl : 0.0f) : rl;
+      norm_row8(h[j], rj, gamma_of(j), y);
       if (p.y != nullptr && live && in)
         *reinterpret_cast<uint4*>(p.y + r * p.cols + 8 * v) =
             make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y),

@@ -57,3 +57,21 @@ def test_padding_is_what_quantising_zero_rows_gives(kind, wgrad, rows, cols, res
         yp = np.zeros((padded, cols), dtype=np.float32)
         yp[:rows] = y
         assert np.array_equal(from_dev_bf16(q.col), bf16_bits_from_f32(np.ascontiguousarray(yp.T)))
+
+
+@pytest.mark.parametrize("kind", ["tensorwise", "delayed"])
+@pytest.mark.parametrize("cols", [16, 48, 2064, 4096, 8208])
+@pytest.mark.parametrize("col", [True, False])
+def test_amax_of_infinities(kind, cols, col):
+    """eps 0 and rows so small that their squares vanish in fp32: rstd is infinite and the
+    outputs infinities. The lanes that have no column in a row of such a width add no NaN."""
+    rec = F.Recipe(kind=kind)
+    x = torch.full((16, cols), 1e-25, dtype=torch.bfloat16, device="cuda")
+    q, _, rstd, y = F.rmsnorm_quantize(rec, x, torch.ones(cols, device="cuda"), eps=0.0,
+                                       want_col=col, want_y=True)
+    torch.cuda.synchronize()
+    assert bool(torch.isinf(rstd).all()) and bool(torch.isinf(y).all())
+    assert q.amax.item() == float("inf")
+    x[3, 5] = 0.0                                   # 0 inf: a NaN of the row's own
+    q = F.rmsnorm_quantize(rec, x, torch.ones(cols, device="cuda"), eps=0.0, want_col=col)[0]
+    assert q.amax.isnan().item()
