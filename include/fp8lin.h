@@ -412,8 +412,9 @@ size_t fp8_rmsnorm_workspace_bytes(const fp8_recipe *recipe, int64_t rows, int64
  * A row's h, rstd, y and row copy do not depend on the other rows nor on their number (per-tensor
  * scales aside).
  * NaN in y gives code 0x7F. A NaN in a row of h makes the whole row NaN. An infinity, or squares
- * whose sum leaves fp32's range (|h| of 2^63 and more), make the row's rstd 0: its finite elements
- * become zeros, the infinite ones NaN. Apart from h no output may overlap an input.
+ * whose sum over the row leaves fp32's range (2^128: |h| of 2^64 / sqrt(cols) where all are alike,
+ * 2^58 for 4096 columns), make the row's rstd 0: its finite elements become zeros, the infinite ones
+ * NaN. Apart from h no output may overlap an input.
  * Source: the norm in front of each linear layer of the transformer block that the "Low-Precision
  * Training Guide" trains (section "When to Use Low Precision"); the formulas and the fusion are
  * this library's.

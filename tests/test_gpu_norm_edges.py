@@ -6,7 +6,7 @@ import torch
 
 from helpers import cuda_ok, from_dev_bf16, to_dev_bf16
 from oracle import fp8_oracle as O
-from test_gpu_norm import check_copies
+from test_gpu_norm import RSTD_RTOL, check_copies
 from workloads import bf16_bits_from_f32, bf16_bits_normal
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +75,24 @@ def test_amax_of_infinities(kind, cols, col):
     x[3, 5] = 0.0                                   # 0 inf: a NaN of the row's own
     q = F.rmsnorm_quantize(rec, x, torch.ones(cols, device="cuda"), eps=0.0, want_col=col)[0]
     assert q.amax.isnan().item()
+
+
+@pytest.mark.parametrize("cols,below,above", [(128, 181 / 128 * 2.0 ** 60, 182 / 128 * 2.0 ** 60),
+                                              (4096, 255 / 128 * 2.0 ** 57, 2.0 ** 58),
+                                              (32768, 181 / 128 * 2.0 ** 56,
+                                               182 / 128 * 2.0 ** 56)])
+def test_range_of_a_rows_squares(cols, below, above):
+    """The last bf16 value before cols squares add up to 2^128, and the next one (in bf16, 181/128
+    lies just below the root of 2): the formula's value, then rstd 0 and zeros. One element may be
+    larger, as long as its square is in range."""
+    assert cols * below ** 2 < 2.0 ** 128 <= cols * above ** 2
+    x = torch.zeros(3, cols, dtype=torch.bfloat16, device="cuda")
+    x[0], x[1], x[2, 7] = below, above, 2.0 ** 63
+    assert float(x[0, 0]) == below and float(x[1, 0]) == above
+    y, _, rstd = F.rmsnorm(x, torch.ones(cols, device="cuda"))
+    torch.cuda.synchronize()
+    r = rstd.cpu().numpy().astype(np.float64)
+    for i, ref in ((0, 1 / below), (2, cols ** 0.5 * 2.0 ** -63)):
+        assert abs(r[i] - ref) <= RSTD_RTOL * ref
+    assert bool((y[0] == 1).all()) and y[2, 7].item() == torch.tensor(cols ** 0.5).bfloat16().item()
+    assert r[1] == 0 and not y[1].any()
