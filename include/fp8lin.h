@@ -393,7 +393,8 @@ size_t fp8_rmsnorm_workspace_bytes(const fp8_recipe *recipe, int64_t rows, int64
  *              column copy is the bf16 transpose of bf16(y)). May be NULL when neither copy is
  *              wanted: then only y_bf16 (and h, rstd) are written.
  *   in         the inputs. rows is any number >= 0 (a single token when serving); cols is a
- *              multiple of 16, and of 128 for MXFP8 and BLOCKWISE, at most 32768.
+ *              multiple of 16, and of 128 for MXFP8 and BLOCKWISE, at most 32768. Without columns
+ *              or rows nothing is written but the per-tensor amax and scales of an empty tensor.
  *   h_bf16     [rows][cols] bf16, contiguous: the new residual stream. Required with a
  *              residual, not written (may be NULL) without. May be in->x or in->residual
  *              itself when that is contiguous (an update in place).
@@ -446,6 +447,8 @@ size_t fp8_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  *   xh = h * rstd,  t = dy * gamma,  c[r] = mean_c(t * xh)
  *   dh = bf16(dres + rstd * (t - xh * c))      the gradient of x and of residual alike
  *   dgamma[c] = sum_r dy * xh                  fp32, a fixed order of additions
+ * The order of a row's and a column's additions follows from the numbers of rows and columns: equal
+ * calls give equal bits, but a row's dh may differ in its last bit in a batch of another size.
  *   dh_bf16    [rows][cols] bf16, contiguous; may be in->dy or in->dres itself when that is
  *              contiguous.
  *   dgamma     [cols] fp32, 16-byte aligned, overwritten (zeros when rows is 0), or NULL.
@@ -490,9 +493,10 @@ size_t fp8_grad_workspace_bytes(int32_t n);
  *   items      n descriptions in host memory, read during the call only (n >= 0).
  *   norm, coef device fp32 scalars; coef may be NULL.
  *   workspace  fp8_grad_workspace_bytes(n) of device scratch.
- * Squares are added in fp32 in a fixed order, so equal inputs give equal bits, and the sums of
- * blocks in fp64; values whose squares leave fp32's range are squared in fp64. An infinite or
- * NaN gradient makes the norm infinite or NaN, and coef 0 or NaN: the caller looks at the norm.
+ * Squares are added in fp32 in an order that the tensors' sizes and alignment fix, so equal calls
+ * give equal bits, and the sums of blocks in fp64; values whose squares leave fp32's range are squared in fp64. An infinite or
+ * NaN gradient makes the norm infinite or NaN, and coef 0 or NaN (scale where max_norm is
+ * infinite): the caller looks at the norm.
  */
 fp8_status fp8_grad_norm(int32_t n, const fp8_grad_item *items, const fp8_clip_rule *rule,
                          float *norm, float *coef, void *workspace, size_t ws_bytes,

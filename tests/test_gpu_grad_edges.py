@@ -44,3 +44,16 @@ def test_the_norm_of_long_lists_has_no_bias(dtype, numel):
         ref = math.sqrt(sum(float(p.double().square().sum()) for p in g.split(1 << 26)))
         errors.append(F.grad_norm([g])[0].item() / ref - 1)
     assert abs(sum(errors) / len(errors)) <= 2.0 ** -24
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("numel", [100, 700001])
+def test_coefficient_of_a_norm_that_is_not_finite(bad, numel):
+    """0 or NaN, or the scale where nothing is to be clipped."""
+    g = torch.full((numel,), 1e-3, device="cuda")
+    g[-1] = bad
+    norm, coef = F.grad_norm([g], scale=0.5)
+    assert norm.isnan().item() == math.isnan(bad) and not torch.isfinite(norm).item()
+    assert coef.item() == 0.5
+    _, coef = F.grad_norm([g], max_norm=1.0, scale=0.5)
+    assert coef.isnan().item() if math.isnan(bad) else coef.item() == 0
