@@ -6,7 +6,7 @@ import torch
 
 from helpers import cuda_ok, from_dev_bf16, to_dev_bf16
 from oracle import fp8_oracle as O
-from test_gpu_norm import RSTD_RTOL, check_copies
+from test_gpu_norm import RSTD_RTOL, check_bwd, check_copies, check_norm
 from workloads import bf16_bits_from_f32, bf16_bits_normal
 
 pytestmark = pytest.mark.gpu
@@ -96,3 +96,55 @@ def test_range_of_a_rows_squares(cols, below, above):
         assert abs(r[i] - ref) <= RSTD_RTOL * ref
     assert bool((y[0] == 1).all()) and y[2, 7].item() == torch.tensor(cols ** 0.5).bfloat16().item()
     assert r[1] == 0 and not y[1].any()
+
+
+def _steps(rows, cols, threads_per_row, per_sm):
+    """Rows that each group of threads of the row kernel walks, from its launch: CTAs of 256
+    threads, as many per SM as run at once."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    return rows / (256 // threads_per_row * per_sm * sms)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols,residual,ahead", [(66001, 128, False, 4), (40003, 128, True, 2),
+                                                      (33005, 256, False, 4), (20007, 256, True, 2),
+                                                      (16009, 512, False, 2), (17001, 512, True, 1)])
+def test_groups_that_walk_many_rows(kind, rows, cols, residual, ahead):
+    """Several rows are on their way to a group of threads at once; its ring of buffers comes
+    round twice at least, and ends on a ragged row."""
+    assert _steps(rows, cols, 16 if cols == 128 else 32, 3) > 2 * ahead
+    check_norm(kind, rows, cols, residual=residual, col=kind != "mxfp8")
+
+
+@pytest.mark.parametrize("rows,residual", [(66001, False), (40003, True)])
+def test_narrow_groups_that_walk_many_rows(rows, residual):
+    """Two of a row's sixteen threads have columns."""
+    assert _steps(rows, 16, 16, 3) > (8 if not residual else 4)
+    for kind in ("tensorwise", "delayed"):
+        check_norm(kind, rows, 16, residual=residual)
+    x = to_dev_bf16(bf16_bits_normal(rows, 16, seed=2))
+    res = to_dev_bf16(bf16_bits_normal(rows, 16, seed=3)) if residual else None
+    g = torch.rand(16, device="cuda") + 0.5
+    y, h, rstd = F.rmsnorm(x, g, res)
+    torch.cuda.synchronize()
+    want = O.rmsnorm_y_f32(from_dev_bf16(h), rstd.cpu().numpy(), g.cpu().numpy())
+    assert np.array_equal(from_dev_bf16(y), bf16_bits_from_f32(want))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(256, 32768), (2048, 4096), (1000, 8192)])
+def test_column_blocks_that_walk_whole_tiles(kind, rows, cols):
+    """More tiles of rows than CTAs for a column block, in the kernel that tests nothing per row:
+    whole tiles, and a last one of which some rows are padding (per-tensor recipes pad to 16 rows
+    only: their ragged case runs the general kernel)."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert (rows + 127) // 128 > max(1, 6 * sms // (cols // 64))
+    check_norm(kind, rows, cols, residual=rows != 2048)
+
+
+@pytest.mark.parametrize("rows,cols", [(330, 8192), (400, 16384), (350, 32768)])
+def test_backward_of_wide_rows_that_follow_each_other(rows, cols):
+    """One CTA per SM holds a row of these widths; each walks two or three."""
+    assert rows > 2 * torch.cuda.get_device_properties(0).multi_processor_count
+    check_bwd(rows, cols)
+    check_bwd(rows, cols, dres=False, gamma_fp32=True)
