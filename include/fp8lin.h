@@ -414,8 +414,8 @@ size_t fp8_rmsnorm_workspace_bytes(const fp8_recipe *recipe, int64_t rows, int64
  * scales aside).
  * NaN in y gives code 0x7F. A NaN in a row of h makes the whole row NaN. An infinity, or squares
  * whose sum over the row leaves fp32's range (2^128: |h| of 2^64 / sqrt(cols) where all are alike,
- * 2^58 for 4096 columns), make the row's rstd 0: its finite elements become zeros, the infinite ones
- * NaN. Apart from h no output may overlap an input.
+ * 2^58 for 4096 columns), make the row's rstd 0: its finite elements become zeros, the infinite
+ * ones NaN. Apart from h no output may overlap an input.
  * Source: the norm in front of each linear layer of the transformer block that the "Low-Precision
  * Training Guide" trains (section "When to Use Low Precision"); the formulas and the fusion are
  * this library's.
@@ -494,9 +494,9 @@ size_t fp8_grad_workspace_bytes(int32_t n);
  *   norm, coef device fp32 scalars; coef may be NULL.
  *   workspace  fp8_grad_workspace_bytes(n) of device scratch.
  * Squares are added in fp32 in an order that the tensors' sizes and alignment fix, so equal calls
- * give equal bits, and the sums of blocks in fp64; values whose squares leave fp32's range are squared in fp64. An infinite or
- * NaN gradient makes the norm infinite or NaN, and coef 0 or NaN (scale where max_norm is
- * infinite): the caller looks at the norm.
+ * give equal bits, and the sums of blocks in fp64; values whose squares leave fp32's range are
+ * squared in fp64. An infinite or NaN gradient makes the norm infinite or NaN, and coef 0 or NaN
+ * (scale where max_norm is infinite): the caller looks at the norm.
  */
 fp8_status fp8_grad_norm(int32_t n, const fp8_grad_item *items, const fp8_clip_rule *rule,
                          float *norm, float *coef, void *workspace, size_t ws_bytes,

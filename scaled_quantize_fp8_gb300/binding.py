@@ -432,37 +432,52 @@ def _gamma(gamma: torch.Tensor, cols: int):
     return 1 if dtype is _FP32 else 0
 
 
-def _check_copy(codes, scale, shape, size, block):
-    """A copy's buffers before the kernels write it: codes of `size` bytes in the copy's shape, and
-    for block scales as many bytes as they take, one for 32 codes (four for 128 come to the same).
-    Returns whether they lie on the GPU."""
-    if codes is None or codes.shape != shape or codes.itemsize != size \
-            or not codes.is_contiguous():
-        raise ValueError(f"out: contiguous copies of shape {shape} with {size} bytes an element")
-    if not block or scale is None:                 # (the library refuses scales that are missing)
-        return codes.is_cuda
-    if scale.nbytes < shape[0] * shape[1] // 32 or not scale.is_contiguous():
-        raise ValueError(f"out: contiguous scales of a copy of shape {shape}")
-    return codes.is_cuda and scale.is_cuda
+def _bad_copy(shape, size):
+    raise ValueError(f"out: contiguous copies of shape {shape} with {size} bytes an element, and "
+                     "their scales")
 
 
-def _check_out(out: QTensor, recipe: Recipe, rows, cols, want_row, want_col):
-    """The buffers of a caller's `out`: as empty_qtensor makes them for an activation of `rows`
-    padded rows under this recipe. Returns whether they lie on the GPU."""
-    block = recipe.kind in ("mxfp8", "blockwise")
+def _packed_out(out: QTensor, recipe: Recipe, rows, cols, want_row, want_col, block):
+    """The wanted buffers of `out` in the library's form, checked before the kernels write them:
+    as empty_qtensor makes them for an activation of `rows` padded rows under this recipe. Codes
+    take one byte, the column copy without FP8 wgrad two (and no scales); block scales one byte
+    for 32 codes (four for 128 come to the same). What is missing the library refuses. Returns
+    the structure and whether all of it lies on the GPU."""
+    row = col = row_scale = col_scale = amax = scale = scale_inv = 0
     on_gpu = True
     if want_row:
-        on_gpu = _check_copy(out.row, out.row_scale, (rows, cols), 1, block)
-    if want_col:                                   # without FP8 wgrad in bf16, and no scales
-        fp8 = recipe.fp8_wgrad
-        on_gpu &= _check_copy(out.col, out.col_scale, (cols, rows), 1 if fp8 else 2, block and fp8)
+        t = out.row
+        if t is None or t.shape != (rows, cols) or t.itemsize != 1 or not t.is_contiguous():
+            _bad_copy((rows, cols), 1)
+        row, on_gpu = t.data_ptr(), t.is_cuda
+        t = out.row_scale
+        if block and t is not None:
+            if t.nbytes * 32 < rows * cols or not t.is_contiguous():
+                _bad_copy((rows, cols), 1)
+            row_scale, on_gpu = t.data_ptr(), on_gpu and t.is_cuda
+    if want_col:
+        t, size = out.col, 1 if recipe.fp8_wgrad else 2
+        if t is None or t.shape != (cols, rows) or t.itemsize != size or not t.is_contiguous():
+            _bad_copy((cols, rows), size)
+        col, on_gpu = t.data_ptr(), on_gpu and t.is_cuda
+        t = out.col_scale
+        if block and size == 1 and t is not None:
+            if t.nbytes * 32 < rows * cols or not t.is_contiguous():
+                _bad_copy((cols, rows), 1)
+            col_scale, on_gpu = t.data_ptr(), on_gpu and t.is_cuda
     if not block:
-        for t in (out.amax, out.scale, out.scale_inv):
+        a, s, i = out.amax, out.scale, out.scale_inv
+        for t in (a, s, i):
             if t is not None:
-                if t.dtype is not _FP32 or t.numel() == 0:
+                if t.nbytes < 4:
                     raise ValueError("out: fp32 amax, scale and scale_inv")
-                on_gpu &= t.is_cuda
-    return on_gpu
+                on_gpu = on_gpu and t.is_cuda
+        amax = 0 if a is None else a.data_ptr()
+        scale = 0 if s is None else s.data_ptr()
+        scale_inv = 0 if i is None else i.data_ptr()
+    ct = L.Tensor()
+    L.pack_tensor(ct, 0, row, col, row_scale, col_scale, amax, scale, scale_inv, 0, 0, 0, 0, 0)
+    return ct, on_gpu
 
 
 def rmsnorm_workspace_bytes(recipe: Recipe, rows, cols):
@@ -482,7 +497,8 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
     (out, h, rstd, y): `out` holds the copies of the output padded with rows of zeros to the
     recipe's row quantum (out.rows), h the new residual stream (x itself without a residual),
     rstd fp32 [rows] for rmsnorm_bwd, y the bf16 output (with want_y). Buffers that are not
-    given are allocated; for delayed scaling `out` is bound to its DelayedState."""
+    given are allocated; an `out` that is given has buffers as empty_qtensor makes them for this
+    recipe, and for delayed scaling is bound to its DelayedState."""
     lib = L.load()
     shape = x.shape
     if len(shape) != 2:
@@ -514,16 +530,16 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
     rc = out_ref = None
     on_gpu = True
     if want_row or want_col:
-        q = 128 if recipe.kind in ("mxfp8", "blockwise") else 16
+        block = recipe.kind in ("mxfp8", "blockwise")
+        q = 128 if block else 16
         padded = -(-rows // q) * q
         if out is None:
             with torch.cuda.stream(stream):
                 out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
                                     device=x.device)
-        else:
-            on_gpu = _check_out(out, recipe, padded, cols, want_row, want_col)
-        ct = out.c()
-        out_ref, rc = ctypes.byref(ct), L.pack_recipe(*recipe._fields())
+        ct, on_gpu = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
+        fields = recipe._fields()
+        out_ref, rc = ctypes.byref(ct), L.pack_recipe(*fields)
     if not (on_gpu and x.is_cuda and gamma.is_cuda and h.is_cuda and rstd.is_cuda
             and (residual is None or residual.is_cuda) and (y is None or y.is_cuda)
             and (workspace is None or workspace.is_cuda)):
@@ -539,8 +555,8 @@ def rmsnorm_quantize(recipe: Optional[Recipe], x: torch.Tensor, gamma: torch.Ten
     if st:
         L.check(st, "fp8_rmsnorm_quantize")
     if out_ref is not None:
-        out.rows, out.cols, out.kind, out.role, out.col_bf16 = (padded, cols, ct.kind, ct.role,
-                                                                ct.col_bf16)
+        out.rows, out.cols, out.kind, out.role = padded, cols, fields[0], L.ROLE_ACTIVATION
+        out.col_bf16 = 1 - fields[5]                       # as the library sets them
     return out, h, rstd, y
 
 
@@ -633,10 +649,10 @@ class GradList:
     """The gradients of a step as fp8_grad_norm and fp8_grad_clip take them: bf16 or fp32 CUDA
     tensors of any shape, dense in memory, on one device. `outs` are the tensors that
     grad_clip writes (the gradients themselves when not given), with the gradients' shapes and
-    order in memory. The list holds the tensors' addresses: it is made once for gradients that stay in
-    place, and anew for new tensors. It also holds the results of grad_norm, `norm` and `coef`,
-    which come from the pool of `stream` (the current one if not given): a list whose calls run on
-    another stream is made for that one, or its making is waited for there."""
+    order in memory. The list holds the tensors' addresses: it is made once for gradients that
+    stay in place, and anew for new tensors. It also holds the results of grad_norm, `norm` and
+    `coef`, which come from the pool of `stream` (the current one if not given): a list whose
+    calls run on another stream is made for that one, or its making is waited for there."""
 
     def __init__(self, grads, outs=None, stream=None):
         self.grads = list(grads)

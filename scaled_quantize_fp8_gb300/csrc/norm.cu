@@ -91,14 +91,15 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
   return m;
 }
 
-// ------------------------------------------------------------------------- rows tpr threads per
-// row (16, or a multiple of 32), V 16-byte vectors a thread; vector j of lane l holds columns 8 (j
-// tpr + l) ..  so a warp reads 512 consecutive bytes and a block of 32 (128) columns lies in 4
-// (16) neighbouring lanes. The CTAs stay and walk the rows; each thread copies its own elements of
-// the next row to shared memory (cp.async) while it works on the present one, and gamma stays in
-// registers. Sums of squares in fp32, two a thread, then over lanes and warps in a fixed order. y
-// is made twice, for the maxima and for the codes: kept in between, two vectors are no faster
-// (39.0 us either way, measured at that time) and four spill.
+// ------------------------------------------------------------------------- rows
+// tpr threads per row (16, or a multiple of 32), V 16-byte vectors a thread; vector j of lane l
+// holds columns 8 (j tpr + l) .. so a warp reads 512 consecutive bytes and a block of 32 (128)
+// columns lies in 4 (16) neighbouring lanes. The CTAs stay and walk the rows; each thread copies
+// its own elements of the next row to shared memory (cp.async) while it works on the present one,
+// and gamma stays in registers (up to four vectors). Sums of squares in fp32, two a thread, then
+// over lanes and warps in a fixed order. y is made twice, for the maxima and for the codes: kept
+// in between, two vectors are no faster (39.0 us either way, measured at that time) and four
+// spill.
 //
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 37.7 us, 6260
 // GB/s); without one the instructions as much (20.6 us for 15.0 of memory, of which the second sum
@@ -667,7 +668,8 @@ constexpr int kNormMaxParts = 4096;   // amax partials: one per CTA of the row k
 // Vectors a thread: enough loads in flight, but no more registers than that needs. With a residual
 // (twice the loads) two, 4096 columns then being 256 threads (8192 x 4096, row copy: 37.7 us; four
 // 39.2, one 47.1); without one four (both copies: 33.6; two 36.9); and four for longer rows, of
-// which two would make CTAs of 512 threads, one per SM (4096 x 8192, row copy: 38.0; two 42.2).
+// which two would make CTAs of 512 threads, one per SM (4096 x 8192, row copy: 38.0; two 42.2;
+// widths between the two were not measured).
 // A row's sum, and so its last bit, must not depend on how many rows there are (a token served
 // alone gives what it gives in a batch) nor on whether the residual was added here: the threads
 // are twice as many with two vectors, which are used only where that comes out even, and few rows,

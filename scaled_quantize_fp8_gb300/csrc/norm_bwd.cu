@@ -167,8 +167,8 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
     if (kBufs == 1 && r + step - grp < p.rows) prefetch(r + step, 0);
   }
   if (p.part != nullptr) {
-    // the groups' sums, added by the first group in order (slots: 64 V nt bytes or more, of
-    // which 32 V nt are used here)
+    // the groups' sums, added by the first group in order (slots: 64 V nt bytes or more up to
+    // four vectors a thread, of which 32 V nt are used here; with eight there is one group)
     float4* sums = reinterpret_cast<float4*>(slots);
     if (rpc > 1) {
       __syncthreads();

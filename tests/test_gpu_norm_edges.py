@@ -106,9 +106,9 @@ def _steps(rows, cols, threads_per_row, per_sm):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("rows,cols,residual,ahead", [(66001, 128, False, 4), (40003, 128, True, 2),
-                                                      (33005, 256, False, 4), (20007, 256, True, 2),
-                                                      (16009, 512, False, 2), (17001, 512, True, 1)])
+@pytest.mark.parametrize("rows,cols,residual,ahead",
+                         [(66001, 128, False, 4), (40003, 128, True, 2), (33005, 256, False, 4),
+                          (20007, 256, True, 2), (16009, 512, False, 2), (17001, 512, True, 1)])
 def test_groups_that_walk_many_rows(kind, rows, cols, residual, ahead):
     """Several rows are on their way to a group of threads at once; its ring of buffers comes
     round twice at least, and ends on a ragged row."""
