@@ -102,7 +102,7 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // spill.
 //
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 37.7 us, 6260
-// GB/s); without one the instructions as much (20.6 us for 15.0 of memory, of which the second sum
+// GB/s); without one the instructions as much (21.4 us for 15.0 of memory, of which the second sum
 // over the lanes, see there, is 1.2).
 
 // Reduce the V vectors' values over the lanes that differ in the bits OFF .. 1: as long as there
