@@ -459,6 +459,95 @@ fp8_status fp8_rmsnorm_bwd(const fp8_norm_grad *in, void *dh_bf16, float *dgamma
                            size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
 
 /*
+ * Activations kept for the backward pass in 8 bits: half the memory and traffic of bf16. A
+ * checkpoint of a bf16 tensor [rows][cols] (cols a multiple of 16) is
+ *
+ *   codes  [rows][cols] E4M3, contiguous
+ *   scale  [rows][4 ceil(cols / 128)] E8M0: the byte of row r's columns 32 b .. 32 b + 31 at
+ *          r * 4 ceil(cols / 128) + b. Bytes of blocks beyond the columns are 0.
+ *
+ * by the rules of an MXFP8 row copy (a 1x32 block's exponent is the smallest e with amax <=
+ * 448 * 2^e; a block with an infinity or a NaN has byte 0xFF, codes encode(x) with NaN -> 0x7F, and
+ * reads back as NaN), but with the scales in the row's order and any number of rows. A value read
+ * back is code * 2^e: within 2^-4 of the value, relatively, down to 2^-6 * 2^e.
+ * Both pointers 16-byte aligned.
+ */
+typedef struct {
+  uint8_t *codes;
+  uint8_t *scale;
+} fp8_checkpoint;
+
+/* Bytes of a checkpoint's scales. */
+size_t fp8_checkpoint_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * fp8_checkpoint_write — bf16 [rows][cols], row pitch ldx (elements, a multiple of 8, >= cols) ->
+ * checkpoint. rows >= 0, cols a multiple of 16, at most 2^30.
+ * Source: the MegaDLMs summary "Benefits of Using FP8 Precision with MegaDLMs and Required
+ * Hardware", section "Memory and Storage Optimization" (activations stored in FP8 for the backward
+ * pass); the format is this library's.
+ */
+fp8_status fp8_checkpoint_write(const void *x_bf16, int64_t ldx, int64_t rows, int64_t cols,
+                                const fp8_checkpoint *out, cudaStream_t stream);
+
+/* fp8_checkpoint_read — checkpoint -> bf16 [rows][cols], contiguous; each value rounded once
+ * (exact but where it leaves bf16's range). */
+fp8_status fp8_checkpoint_read(const fp8_checkpoint *in, int64_t rows, int64_t cols, void *x_bf16,
+                               cudaStream_t stream);
+
+/*
+ * The end of one block and the start of the next, for blocks with a norm on both sides (or only in
+ * front), a gate and a residual scale:
+ *
+ *   xo = branch * rstd_branch,  rstd_branch[r] = 1 / sqrt(mean_c branch[r][c]^2 + eps_post)
+ *   h  = bf16(residual + (xo * token_gate[r]) * w[c]),  w[c] = gamma_post[c] * gate[c] * scale
+ *   rstd[r] = 1 / sqrt(mean_c h[r][c]^2 + eps),  y = (h * rstd) * gamma
+ *
+ * in fp32, with one rounding to bf16 at h: the stream is held in bf16 and the norm is taken of it
+ * as stored, as by fp8_rmsnorm_quantize. Without gamma_post there is no norm after the block (xo =
+ * branch, no factor gamma_post); gate and token_gate are factors of 1 where they are NULL.
+ * A token whose token_gate is 0 passes the block by: its h is its residual, whatever its row of
+ * branch holds (it may never have been written).
+ */
+typedef struct {
+  const void *branch;        /* [rows][cols] bf16, row pitch ld_branch: the block's output */
+  const void *residual;      /* [rows][cols] bf16, row pitch ld_residual: the stream before it */
+  const void *gamma_post;    /* [cols] or NULL: weight of the norm after the block */
+  const void *gate;          /* [cols] or NULL: a gate per channel */
+  const float *token_gate;   /* [rows] or NULL: a gate per token (4-byte aligned) */
+  const void *gamma;         /* [cols]: weight of the norm in front of the next block */
+  int64_t ld_branch, ld_residual;   /* pitches in elements, multiples of 8, >= cols */
+  int64_t rows, cols;
+  int32_t gamma_post_fp32, gate_fp32, gamma_fp32;   /* each: bf16 (0) or fp32 (1) */
+  float scale;               /* the residual scale; finite */
+  float eps_post, eps;       /* >= 0 and finite, as fp8_norm_input's eps */
+} fp8_branch_input;
+
+/*
+ * fp8_branch_rmsnorm_quantize — the block's output into the stream, and the FP8 copies of the norm
+ * that follows.
+ *   recipe, want_row, want_col, y_bf16, out, workspace (fp8_rmsnorm_workspace_bytes),
+ *   dev_status, the shapes, the padding and the refusals: as for fp8_rmsnorm_quantize.
+ *   h_bf16        [rows][cols] bf16, contiguous: the new stream. May be in->branch or in->residual
+ *                 itself when that is contiguous.
+ *   rstd_branch   [rows] fp32 for the backward pass, or NULL (not written without gamma_post).
+ *   rstd          [rows] fp32 or NULL.
+ *   branch_ckpt, h_ckpt: checkpoints of branch and of h, written in the same pass; or NULL.
+ * A row's results do not depend on the other rows nor on their number (per-tensor scales aside).
+ * Infinities, NaN and squares beyond fp32's range act as in fp8_rmsnorm_quantize, in either norm.
+ * Apart from h no output may overlap an input or another output.
+ * Source: the transformer block that the "Low-Precision Training Guide" trains (section "When to
+ * Use Low Precision") around its linear layers; the formulas and the fusion are this library's.
+ */
+fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe *recipe, const fp8_branch_input *in,
+                                       int32_t want_row, int32_t want_col, void *h_bf16,
+                                       float *rstd_branch, float *rstd, void *y_bf16,
+                                       const fp8_checkpoint *branch_ckpt,
+                                       const fp8_checkpoint *h_ckpt, fp8_tensor *out,
+                                       void *workspace, size_t ws_bytes, int32_t *dev_status,
+                                       cudaStream_t stream);
+
+/*
  * The gradients of a step, before the optimizer: their global norm and clipping by it.
  *   norm = scale * sqrt(sum over all tensors of g^2)
  *   coef = scale * min(1, max_norm / (norm + 1e-6))

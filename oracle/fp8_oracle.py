@@ -568,6 +568,58 @@ def rmsnorm_bwd_f64(dy, h, rstd, gamma, dres=None):
     return dh, np.sum(dy * xh, axis=0)
 
 
+def _columns_f64(v):
+    return 1.0 if v is None else np.asarray(v, dtype=np.float64)
+
+
+def _rows_f64(v):
+    return 1.0 if v is None else np.asarray(v, dtype=np.float64)[:, None]
+
+
+def branch_sum_f64(branch, residual, rstd_branch=None, gamma_post=None, gate=None,
+                   token_gate=None, scale=1.0):
+    """The stream after a block, before its rounding, float64: residual + scale gate token_gate
+    gamma_post xo with xo = branch rstd_branch (branch itself without a norm after the block)."""
+    xo = np.asarray(branch, dtype=np.float64) * _rows_f64(rstd_branch)
+    return (np.asarray(residual, dtype=np.float64)
+            + float(scale) * _columns_f64(gate) * _rows_f64(token_gate)
+            * _columns_f64(gamma_post) * xo)
+
+
+def branch_bwd_f64(dh, branch, rstd_branch=None, gamma_post=None, gate=None, token_gate=None,
+                   scale=1.0):
+    """Gradients of branch_sum_f64 with rstd_branch taken from branch, for a gradient dh of the
+    stream, float64: {"dbranch", "dgamma_post", "dgate", "dtoken_gate"}."""
+    dh, o = np.asarray(dh, dtype=np.float64), np.asarray(branch, dtype=np.float64)
+    r, t = _rows_f64(rstd_branch), _rows_f64(token_gate)
+    g, a, s = _columns_f64(gate), _columns_f64(gamma_post), float(scale)
+    xo = o * r
+    u = s * t * g * a * dh                               # the gradient of xo
+    if rstd_branch is not None:
+        d = r * (u - xo * np.mean(u * xo, axis=1, keepdims=True))
+    else:
+        d = u
+    return {"dbranch": d, "dgamma_post": np.sum(s * t * g * dh * xo, axis=0),
+            "dgate": np.sum(s * t * a * dh * xo, axis=0),
+            "dtoken_gate": np.sum(s * g * a * dh * xo, axis=1)}
+
+
+def checkpoint_pack(x):
+    """(codes [rows, cols], E8M0 bytes [rows, 4 ceil(cols / 128)]) of an 8-bit checkpoint of bf16
+    bits or float32 values: an MXFP8 row copy (1x32 blocks) with its scales in the row's order."""
+    x = np.asarray(x)
+    rows, cols = x.shape
+    wide = np.zeros((-(-rows // 128) * 128, -(-cols // 128) * 128), dtype=x.dtype)
+    wide[:rows, :cols] = x
+    q = quantize_mxfp8(wide, want_col=False)
+    return q["row"][:rows, :cols], q["row_scale"][:rows]
+
+
+def checkpoint_values(codes, scale):
+    """The values that a checkpoint stands for, float64."""
+    return e4m3_decode(codes) * np.repeat(e8m0_decode(scale), MX_BLOCK, axis=1)[:, :codes.shape[1]]
+
+
 def grad_norm_f64(grads, scale=1.0):
     """scale * the square root of the sum over all tensors of their squares, float64."""
     return float(scale) * math.sqrt(sum(float(np.sum(np.square(np.asarray(g, dtype=np.float64))))

@@ -69,11 +69,28 @@ class NormGrad(ctypes.Structure):
                 ("cols", ctypes.c_int64), ("gamma_fp32", ctypes.c_int32)]
 
 
-# The same two, the clip rule and the norm's recipe as bytes: the binding builds one per call, which
+class Checkpoint(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class BranchInput(ctypes.Structure):
+    _fields_ = [("branch", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("gamma_post", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("token_gate", ctypes.c_void_p), ("gamma", ctypes.c_void_p),
+                ("ld_branch", ctypes.c_int64), ("ld_residual", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("gamma_post_fp32", ctypes.c_int32), ("gate_fp32", ctypes.c_int32),
+                ("gamma_fp32", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("eps_post", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
+# The norms' inputs, the clip rule and the norm's recipe as bytes: the binding builds one per call, which
 # takes half the time of a Structure. The functions take either (their argument is a c_void_p).
 pack_recipe = struct.Struct("@iiiiiii").pack
 pack_norm_input = struct.Struct("@PPPqqqqif").pack
 pack_norm_grad = struct.Struct("@PPPPPqqqqqi4x").pack
+pack_checkpoint = struct.Struct("@PP").pack
+pack_branch_input = struct.Struct("@PPPPPPqqqqiiifff").pack
 pack_clip_rule = struct.Struct("@ff").pack
 
 GRAD_BF16, GRAD_FP32 = 0, 1
@@ -131,6 +148,11 @@ _SIG = {
                                     _P]),
     "fp8_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "fp8_rmsnorm_bwd": (_I32, [_P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "fp8_checkpoint_scale_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "fp8_checkpoint_write": (_I32, [_P, _I64, _I64, _I64, _P, _P]),
+    "fp8_checkpoint_read": (_I32, [_P, _I64, _I64, _P, _P]),
+    "fp8_branch_rmsnorm_quantize": (_I32, [_P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P,
+                                           ctypes.POINTER(Tensor), _P, ctypes.c_size_t, _P, _P]),
     "fp8_grad_workspace_bytes": (ctypes.c_size_t, [_I32]),
     "fp8_grad_norm": (_I32, [_I32, ctypes.POINTER(GradItem), _P, _P, _P, _P,
                              ctypes.c_size_t, _P]),

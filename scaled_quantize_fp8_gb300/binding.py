@@ -624,6 +624,199 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
     return dh, dgamma
 
 
+def _one_device(*tensors):
+    """Every tensor (or None) of a call on the current device, where its kernels run."""
+    here = torch._C._cuda_getDevice() if tensors[0].is_cuda else -1
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            _not_on_gpu() if not t.is_cuda else _other_device()
+    if here < 0:
+        _not_on_gpu()
+
+
+def _other_device():
+    raise ValueError("the tensors of a call lie on the current device")
+
+
+def _columns(t: Optional[torch.Tensor], cols, name: str):
+    """Address and type of an optional bf16 or fp32 vector of [cols]."""
+    if t is None:
+        return 0, 0
+    dtype = t.dtype
+    if dtype is not _BF16 and dtype is not _FP32:
+        raise TypeError(f"{name}: bf16 or fp32")
+    if t.shape != (cols,) or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor of {cols} elements")
+    return t.data_ptr(), 1 if dtype is _FP32 else 0
+
+
+@dataclass
+class Checkpoint:
+    """An activation [rows, cols] kept in 8 bits: uint8 E4M3 codes [rows, cols] and the E8M0 bytes
+    of its blocks of 32 columns, [rows, 4 * ceil(cols / 128)]."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _checkpoint(ck: Checkpoint, shape, name: str):
+    """The checkpoint in the library's form, its buffers checked."""
+    codes, scale = ck.codes, ck.scale
+    want = (shape[0], -(-shape[1] // 128) * 4)
+    if codes.shape != shape or scale.shape != want or codes.itemsize != 1 or scale.itemsize != 1 \
+            or not codes.is_contiguous() or not scale.is_contiguous():
+        raise ValueError(f"{name}: contiguous 8-bit codes {tuple(shape)} and scales {want}")
+    return L.pack_checkpoint(codes.data_ptr(), scale.data_ptr())
+
+
+def empty_checkpoint(rows, cols, device="cuda"):
+    return Checkpoint(torch.empty((rows, cols), dtype=torch.uint8, device=device),
+                      torch.empty((rows, -(-cols // 128) * 4), dtype=torch.uint8, device=device))
+
+
+def checkpoint(x: torch.Tensor, out: Optional[Checkpoint] = None, stream=None):
+    """fp8_checkpoint_write: the checkpoint of a bf16 [rows, cols] tensor, whose rows may be
+    strided; any number of rows, cols a multiple of 16."""
+    if x.dim() != 2:
+        raise TypeError("x: a bf16 [rows, cols] tensor")
+    rows, cols = x.shape
+    ldx = _rows_2d(x, cols, "x")
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = empty_checkpoint(rows, cols, device=x.device)
+    ck = _checkpoint(out, x.shape, "out")
+    _one_device(x, out.codes, out.scale)
+    st = L.load().fp8_checkpoint_write(x.data_ptr(), ldx, rows, cols, ck, _raw_stream(stream))
+    if st:
+        L.check(st, "fp8_checkpoint_write")
+    return out
+
+
+def checkpoint_read(ck: Checkpoint, out: Optional[torch.Tensor] = None, stream=None):
+    """fp8_checkpoint_read: the checkpoint's values as a bf16 tensor."""
+    shape = ck.codes.shape
+    if len(shape) != 2:
+        raise TypeError("codes: a [rows, cols] tensor")
+    c = _checkpoint(ck, shape, "ck")
+    if out is None:
+        out = _empty(shape, _BF16, ck.codes.device, stream)
+    else:
+        _like(out, shape, _BF16, "out")
+    _one_device(ck.codes, ck.scale, out)
+    st = L.load().fp8_checkpoint_read(c, shape[0], shape[1], out.data_ptr(), _raw_stream(stream))
+    if st:
+        L.check(st, "fp8_checkpoint_read")
+    return out
+
+
+def branch_rmsnorm_quantize(recipe: Optional[Recipe], branch: torch.Tensor,
+                            residual: torch.Tensor, gamma: torch.Tensor,
+                            gamma_post: Optional[torch.Tensor] = None,
+                            gate: Optional[torch.Tensor] = None,
+                            token_gate: Optional[torch.Tensor] = None, scale=1.0, eps=1e-5,
+                            eps_post: Optional[float] = None, want_row=True, want_col=True,
+                            want_y=False, out: Optional[QTensor] = None,
+                            h: Optional[torch.Tensor] = None,
+                            rstd: Optional[torch.Tensor] = None,
+                            rstd_branch: Optional[torch.Tensor] = None,
+                            y: Optional[torch.Tensor] = None,
+                            branch_ckpt: Optional[Checkpoint] = None,
+                            h_ckpt: Optional[Checkpoint] = None,
+                            workspace: Optional[torch.Tensor] = None, status=None, stream=None):
+    """fp8_branch_rmsnorm_quantize: h = residual + scale * gate * token_gate * norm(branch), RMSNorm
+    of h and the FP8 copies of its output.
+
+    branch and residual are bf16 [rows, cols], their rows may be strided; any number of rows.
+    gamma_post is the weight of the norm of branch (none without it), gate a factor per channel
+    (both bf16 or fp32 [cols]), token_gate one per row (fp32 [rows]); eps_post is eps where not
+    given. Returns (out, h, rstd, rstd_branch, y) as rmsnorm_quantize does; rstd_branch is None
+    without gamma_post. Checkpoints that are given (as empty_checkpoint makes them) are filled with
+    branch and h for the backward pass. Without a recipe (and copies) y alone is made."""
+    lib = L.load()
+    shape = branch.shape
+    if len(shape) != 2:
+        raise TypeError("branch: a bf16 [rows, cols] tensor")
+    rows, cols = shape
+    ld_branch = _rows_2d(branch, cols, "branch")
+    if residual.shape != shape:
+        raise ValueError("residual: the shape of branch")
+    ld_residual = _rows_2d(residual, cols, "residual")
+    post_ptr, post_fp32 = _columns(gamma_post, cols, "gamma_post")
+    gate_ptr, gate_fp32 = _columns(gate, cols, "gate")
+    token_ptr = 0
+    if token_gate is not None:
+        _like(token_gate, (rows,), _FP32, "token_gate")
+        token_ptr = token_gate.data_ptr()
+    if h is None:
+        h = _empty(shape, _BF16, branch.device, stream)
+    else:
+        _like(h, shape, _BF16, "h")
+    if rstd is None:
+        rstd = _empty(rows, _FP32, branch.device, stream)
+    else:
+        _like(rstd, (rows,), _FP32, "rstd")
+    if gamma_post is None:
+        rstd_branch = None
+    elif rstd_branch is None:
+        rstd_branch = _empty(rows, _FP32, branch.device, stream)
+    else:
+        _like(rstd_branch, (rows,), _FP32, "rstd_branch")
+    if y is not None:
+        _like(y, shape, _BF16, "y")
+    elif want_y:
+        y = _empty(shape, _BF16, branch.device, stream)
+    o_ck = h_ck = None
+    tensors = [branch, residual, gamma, h, rstd, gamma_post, gate, token_gate, rstd_branch, y,
+               workspace]
+    if branch_ckpt is not None:
+        o_ck = _checkpoint(branch_ckpt, shape, "branch_ckpt")
+        tensors += (branch_ckpt.codes, branch_ckpt.scale)
+    if h_ckpt is not None:
+        h_ck = _checkpoint(h_ckpt, shape, "h_ckpt")
+        tensors += (h_ckpt.codes, h_ckpt.scale)
+    inp = L.pack_branch_input(branch.data_ptr(), residual.data_ptr(), post_ptr, gate_ptr,
+                              token_ptr, gamma.data_ptr(), ld_branch, ld_residual, rows, cols,
+                              post_fp32, gate_fp32, _gamma(gamma, cols), scale,
+                              eps if eps_post is None else eps_post, eps)
+    _one_device(*tensors)
+    rc = out_ref = None
+    if want_row or want_col:
+        block = recipe.kind in ("mxfp8", "blockwise")
+        q = 128 if block else 16
+        padded = -(-rows // q) * q
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
+                                    device=branch.device)
+        ct, on_gpu = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
+        if not on_gpu:
+            _not_on_gpu()
+        fields = recipe._fields()
+        out_ref, rc = ctypes.byref(ct), L.pack_recipe(*fields)
+    args = (rc, inp, want_row, want_col, h.data_ptr(),
+            None if rstd_branch is None else rstd_branch.data_ptr(), rstd.data_ptr(),
+            None if y is None else y.data_ptr(), o_ck, h_ck, out_ref)
+    rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
+    st = lib.fp8_branch_rmsnorm_quantize(*args, *_buffer(workspace), *rest)
+    if st == L.FP8_ERR_WORKSPACE:            # none given, or too small: one of the call's own
+        workspace = _empty(lib.fp8_rmsnorm_workspace_bytes(rc, rows, cols), torch.uint8,
+                           branch.device, stream)
+        st = lib.fp8_branch_rmsnorm_quantize(*args, *_buffer(workspace), *rest)
+    if st:
+        L.check(st, "fp8_branch_rmsnorm_quantize")
+    if out_ref is not None:
+        out.rows, out.cols, out.kind, out.role = padded, cols, fields[0], L.ROLE_ACTIVATION
+        out.col_bf16 = 1 - fields[5]                       # as the library sets them
+    return out, h, rstd, rstd_branch, y
+
+
 _GRAD_DTYPES = {torch.bfloat16: L.GRAD_BF16, torch.float32: L.GRAD_FP32}
 
 

@@ -615,6 +615,93 @@ fp8_status check_norm_shape(int64_t rows, int64_t cols, int64_t quantum) {
   return FP8_OK;
 }
 
+// The checks of a call that normalises rows into copies: `a` holds the inputs and outputs; what the
+// recipe says is filled in.
+fp8_status check_norm(const fp8_recipe* recipe, int32_t want_row, int32_t want_col,
+                      const fp8_tensor* out, NormArgs* a, const void* workspace, size_t ws_bytes) {
+  a->quantise = want_row || want_col;
+  if (a->quantise) {
+    FP8_TRY(check_recipe(recipe));
+    if (out == nullptr) return FP8_ERR_NULL;
+    a->kind = recipe->kind;
+    a->margin = recipe->margin;
+    a->pow2 = recipe->power_2_scales != 0;
+    a->want_row = want_row != 0;
+    a->want_col = want_col != 0;
+    a->col_bf16 = recipe->fp8_wgrad == 0;
+  } else if (a->y == nullptr) {
+    return FP8_ERR_SHAPE;                   // nothing to compute
+  }
+  const int64_t rows = a->rows, cols = a->cols;
+  FP8_TRY(check_norm_shape(rows, cols, a->quantise ? shape_quantum(a->kind) : 16));
+  if (a->quantise && norm_pad_rows(a->kind, rows) * cols >= (int64_t(1) << 31))
+    return FP8_ERR_SHAPE;
+  if (!(a->eps >= 0.0f) || a->eps > 3.402823466e38f) return FP8_ERR_UNSUPPORTED;
+  if (a->gamma_fp32 != 0 && a->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
+  if (a->quantise) FP8_TRY(check_scalars(a->kind, out));
+  if (rows == 0 || cols == 0) return FP8_OK;
+  FP8_TRY(check_ptr(a->x));
+  FP8_TRY(check_pitch(a->ldx, cols));
+  FP8_TRY(check_ptr(a->gamma));
+  if (a->res != nullptr) {
+    FP8_TRY(check_ptr(a->res));
+    FP8_TRY(check_pitch(a->ldr, cols));
+    FP8_TRY(check_ptr(a->h));
+    // in place only where h's rows lie on the input's
+    if ((a->h == a->x && a->ldx != cols) || (a->h == a->res && a->ldr != cols))
+      return FP8_ERR_SHAPE;
+  }
+  if (reinterpret_cast<uintptr_t>(a->rstd) % 4 != 0) return FP8_ERR_ALIGN;
+  if (a->y != nullptr) FP8_TRY(check_ptr(a->y));
+  if (a->want_row) FP8_TRY(check_copy(a->kind, out->row, out->row_scale));
+  if (a->want_col) {
+    if (a->col_bf16) FP8_TRY(check_ptr(out->col));
+    else FP8_TRY(check_copy(a->kind, out->col, out->col_scale));
+  }
+  const size_t need = a->quantise ? norm_workspace_bytes(a->kind, rows, cols) : 0;
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
+  return FP8_OK;
+}
+
+void set_norm_out(const NormArgs& a, fp8_tensor* out) {
+  if (!a.quantise) return;
+  out->rows = norm_pad_rows(a.kind, a.rows);
+  out->cols = a.cols;
+  out->role = FP8_ROLE_ACTIVATION;
+  out->kind = a.kind;
+  out->col_bf16 = a.col_bf16 ? 1 : 0;
+}
+
+// No rows or no columns: the per-tensor recipes' amax 0 and its scale.
+fp8_status empty_norm(const NormArgs& a, int32_t want_row, int32_t want_col, fp8_tensor* out,
+                      void* workspace, cudaStream_t stream) {
+  if (!a.quantise) return FP8_OK;
+  return cuda_status(quantize_launch(a.kind, FP8_ROLE_ACTIVATION, 0, false, a.margin, nullptr, 0,
+                                     a.cols, want_row != 0, want_col != 0, a.col_bf16, out,
+                                     workspace, nullptr, stream));
+}
+
+fp8_status check_vector(const void* p, int32_t fp32) {
+  if (fp32 != 0 && fp32 != 1) return FP8_ERR_UNSUPPORTED;
+  return p != nullptr && !aligned16(p) ? FP8_ERR_ALIGN : FP8_OK;
+}
+
+bool finite(float v) { return v - v == 0.0f; }
+
+fp8_status check_checkpoint(const fp8_checkpoint* c) {
+  FP8_TRY(check_ptr(c->codes));
+  return check_ptr(c->scale);
+}
+
+constexpr int64_t kCheckpointMaxCols = int64_t(1) << 30;
+
+fp8_status check_checkpoint_shape(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || cols % 16 != 0 || cols > kCheckpointMaxCols) return FP8_ERR_SHAPE;
+  if (cols > 0 && rows > (int64_t(1) << 40) / cols) return FP8_ERR_SHAPE;
+  return FP8_OK;
+}
+
 fp8_status check_grads(int32_t n, const fp8_grad_item* items, bool outs) {
   if (n < 0) return FP8_ERR_SHAPE;
   if (n > 0 && items == nullptr) return FP8_ERR_NULL;
@@ -652,60 +739,7 @@ fp8_status fp8_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_norm_input* 
                                 void* y_bf16, fp8_tensor* out, void* workspace, size_t ws_bytes,
                                 int32_t* dev_status, cudaStream_t stream) {
   (void)dev_status;                         // no device-side waits in this path
-  const bool quantise = want_row || want_col;
   if (in == nullptr) return FP8_ERR_NULL;
-  if (quantise) {
-    FP8_TRY(check_recipe(recipe));
-    if (out == nullptr) return FP8_ERR_NULL;
-  } else if (y_bf16 == nullptr) {
-    return FP8_ERR_SHAPE;                   // nothing to compute
-  }
-  const int kind = quantise ? recipe->kind : -1;
-  const int64_t rows = in->rows, cols = in->cols;
-  FP8_TRY(check_norm_shape(rows, cols, quantise ? shape_quantum(kind) : 16));
-  const int64_t rows_pad = quantise ? norm_pad_rows(kind, rows) : rows;
-  if (quantise && rows_pad * cols >= (int64_t(1) << 31)) return FP8_ERR_SHAPE;
-  if (!(in->eps >= 0.0f) || in->eps > 3.402823466e38f) return FP8_ERR_UNSUPPORTED;
-  if (in->gamma_fp32 != 0 && in->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
-  if (quantise) FP8_TRY(check_scalars(kind, out));
-  const bool col_bf16 = quantise && recipe->fp8_wgrad == 0;
-  const bool empty = rows == 0 || cols == 0;
-  if (!empty) {
-    FP8_TRY(check_ptr(in->x));
-    FP8_TRY(check_pitch(in->ldx, cols));
-    FP8_TRY(check_ptr(in->gamma));
-    if (in->residual != nullptr) {
-      FP8_TRY(check_ptr(in->residual));
-      FP8_TRY(check_pitch(in->ldr, cols));
-      FP8_TRY(check_ptr(h_bf16));
-      // in place only where h's rows lie on the input's
-      if ((h_bf16 == in->x && in->ldx != cols) || (h_bf16 == in->residual && in->ldr != cols))
-        return FP8_ERR_SHAPE;
-    }
-    if (rstd != nullptr && reinterpret_cast<uintptr_t>(rstd) % 4 != 0) return FP8_ERR_ALIGN;
-    if (y_bf16 != nullptr) FP8_TRY(check_ptr(y_bf16));
-    if (want_row) FP8_TRY(check_copy(kind, out->row, out->row_scale));
-    if (want_col) {
-      if (col_bf16) FP8_TRY(check_ptr(out->col));
-      else FP8_TRY(check_copy(kind, out->col, out->col_scale));
-    }
-    const size_t need = quantise ? norm_workspace_bytes(kind, rows, cols) : 0;
-    if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8_ERR_WORKSPACE;
-    if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
-  }
-  if (quantise) {
-    out->rows = rows_pad;
-    out->cols = cols;
-    out->role = FP8_ROLE_ACTIVATION;
-    out->kind = kind;
-    out->col_bf16 = col_bf16 ? 1 : 0;
-  }
-  if (empty) {                              // per-tensor recipes: amax 0 and its scale
-    if (!quantise) return FP8_OK;
-    return cuda_status(quantize_launch(kind, FP8_ROLE_ACTIVATION, 0, false, recipe->margin,
-                                       nullptr, 0, cols, want_row != 0, want_col != 0, col_bf16,
-                                       out, workspace, nullptr, stream));
-  }
   NormArgs a{};
   a.x = reinterpret_cast<const uint16_t*>(in->x);
   a.res = reinterpret_cast<const uint16_t*>(in->residual);
@@ -713,21 +747,15 @@ fp8_status fp8_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_norm_input* 
   a.gamma_fp32 = in->gamma_fp32;
   a.ldx = in->ldx;
   a.ldr = in->ldr;
-  a.rows = rows;
-  a.cols = cols;
+  a.rows = in->rows;
+  a.cols = in->cols;
   a.eps = in->eps;
   a.h = reinterpret_cast<uint16_t*>(h_bf16);
   a.rstd = rstd;
   a.y = reinterpret_cast<uint16_t*>(y_bf16);
-  a.quantise = quantise;
-  if (quantise) {
-    a.kind = kind;
-    a.margin = recipe->margin;
-    a.pow2 = recipe->power_2_scales != 0;
-    a.want_row = want_row != 0;
-    a.want_col = want_col != 0;
-    a.col_bf16 = col_bf16;
-  }
+  FP8_TRY(check_norm(recipe, want_row, want_col, out, &a, workspace, ws_bytes));
+  set_norm_out(a, out);
+  if (a.rows == 0 || a.cols == 0) return empty_norm(a, want_row, want_col, out, workspace, stream);
   return cuda_status(norm_quantize_launch(a, out, workspace, stream));
 }
 
@@ -790,6 +818,77 @@ fp8_status fp8_grad_clip(int32_t n, const fp8_grad_item* items, const float* coe
   if (reinterpret_cast<uintptr_t>(coef) % 4 != 0) return FP8_ERR_ALIGN;
   FP8_TRY(check_grads(n, items, true));
   return cuda_status(grad_clip_launch(n, items, coef, stream));
+}
+
+// ---- a block's output into the stream, and checkpoints in 8 bits
+
+size_t fp8_checkpoint_scale_bytes(int64_t rows, int64_t cols) {
+  return rows <= 0 || cols <= 0 ? 0 : size_t(rows) * size_t((cols + 127) / 128 * 4);
+}
+
+fp8_status fp8_checkpoint_write(const void* x_bf16, int64_t ldx, int64_t rows, int64_t cols,
+                                const fp8_checkpoint* out, cudaStream_t stream) {
+  if (out == nullptr) return FP8_ERR_NULL;
+  FP8_TRY(check_checkpoint_shape(rows, cols));
+  if (rows == 0 || cols == 0) return FP8_OK;
+  FP8_TRY(check_ptr(x_bf16));
+  FP8_TRY(check_pitch(ldx, cols));
+  FP8_TRY(check_checkpoint(out));
+  return cuda_status(checkpoint_write_launch(reinterpret_cast<const uint16_t*>(x_bf16), ldx, rows,
+                                             cols, *out, stream));
+}
+
+fp8_status fp8_checkpoint_read(const fp8_checkpoint* in, int64_t rows, int64_t cols, void* x_bf16,
+                               cudaStream_t stream) {
+  if (in == nullptr) return FP8_ERR_NULL;
+  FP8_TRY(check_checkpoint_shape(rows, cols));
+  if (rows == 0 || cols == 0) return FP8_OK;
+  FP8_TRY(check_checkpoint(in));
+  FP8_TRY(check_ptr(x_bf16));
+  return cuda_status(checkpoint_read_launch(*in, rows, cols, reinterpret_cast<uint16_t*>(x_bf16),
+                                            stream));
+}
+
+fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_branch_input* in,
+                                       int32_t want_row, int32_t want_col, void* h_bf16,
+                                       float* rstd_branch, float* rstd, void* y_bf16,
+                                       const fp8_checkpoint* branch_ckpt,
+                                       const fp8_checkpoint* h_ckpt, fp8_tensor* out,
+                                       void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                       cudaStream_t stream) {
+  (void)dev_status;                         // no device-side waits in this path
+  if (in == nullptr) return FP8_ERR_NULL;
+  NormArgs a{};
+  a.x = reinterpret_cast<const uint16_t*>(in->branch);
+  a.res = reinterpret_cast<const uint16_t*>(in->residual);
+  a.gamma = in->gamma;
+  a.gamma_fp32 = in->gamma_fp32;
+  a.ldx = in->ld_branch;
+  a.ldr = in->ld_residual;
+  a.rows = in->rows;
+  a.cols = in->cols;
+  a.eps = in->eps;
+  a.h = reinterpret_cast<uint16_t*>(h_bf16);
+  a.rstd = rstd;
+  a.y = reinterpret_cast<uint16_t*>(y_bf16);
+  FP8_TRY(check_norm(recipe, want_row, want_col, out, &a, workspace, ws_bytes));
+  FP8_TRY(check_vector(in->gamma_post, in->gamma_post_fp32));
+  FP8_TRY(check_vector(in->gate, in->gate_fp32));
+  if (!(in->eps_post >= 0.0f) || !finite(in->eps_post) || !finite(in->scale))
+    return FP8_ERR_UNSUPPORTED;
+  const bool empty = a.rows == 0 || a.cols == 0;
+  if (!empty) {
+    if (a.res == nullptr) return FP8_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(in->token_gate) % 4 != 0 ||
+        reinterpret_cast<uintptr_t>(rstd_branch) % 4 != 0)
+      return FP8_ERR_ALIGN;
+    if (branch_ckpt != nullptr) FP8_TRY(check_checkpoint(branch_ckpt));
+    if (h_ckpt != nullptr) FP8_TRY(check_checkpoint(h_ckpt));
+  }
+  set_norm_out(a, out);
+  if (empty) return empty_norm(a, want_row, want_col, out, workspace, stream);
+  return cuda_status(branch_quantize_launch(a, *in, rstd_branch, branch_ckpt, h_ckpt, out,
+                                            workspace, stream));
 }
 
 }  // extern "C"

@@ -149,6 +149,18 @@ size_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 cudaError_t norm_bwd_launch(const fp8_norm_grad& a, uint16_t* dh, float* dgamma, void* workspace,
                             cudaStream_t st);
 
+// ---- branch.cu (a block's output joins the stream; the norm in front of the next)
+// a: x is the block's output, res the stream.
+cudaError_t branch_quantize_launch(const NormArgs& a, const fp8_branch_input& in, float* rstd_o,
+                                   const fp8_checkpoint* o_ckpt, const fp8_checkpoint* h_ckpt,
+                                   fp8_tensor* out, void* workspace, cudaStream_t st);
+
+// ---- checkpoint.cu (activations in 8 bits)
+cudaError_t checkpoint_write_launch(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols,
+                                    const fp8_checkpoint& out, cudaStream_t st);
+cudaError_t checkpoint_read_launch(const fp8_checkpoint& in, int64_t rows, int64_t cols,
+                                   uint16_t* x, cudaStream_t st);
+
 // ---- grad.cu (global gradient norm, clipping)
 size_t grad_workspace_bytes(int n);
 cudaError_t grad_norm_launch(int n, const fp8_grad_item* items, const fp8_clip_rule& rule,

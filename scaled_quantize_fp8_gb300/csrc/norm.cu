@@ -27,70 +27,6 @@
 
 namespace fp8lin {
 
-enum NormOut : int { N_STATS = 0, N_TENSOR = 1, N_MX = 2, N_BW = 3 };
-
-struct NormParams {
-  const uint16_t* x;          // [rows][cols], pitch ldx
-  const uint16_t* res;        // pitch ldr, or null
-  const void* gamma;
-  int64_t ldx, ldr;
-  int64_t rows, rows_pad;     // rows_pad: a multiple of the recipe's row quantum
-  int cols;
-  int gamma_fp32;
-  float eps, inv_cols;
-  uint16_t* h;                // [rows][cols] (written with a residual)
-  float* rstd;                // [rows] or null
-  uint16_t* y;                // [rows][cols] bf16(y) or null
-  uint8_t* row;               // [rows_pad][cols] codes
-  void* row_scale;
-  uint8_t* col;               // [cols][rows_pad] codes, or bf16 with col_bf16
-  void* col_scale;
-  const float* scale_in;      // per-tensor scale to cast with (delayed), or null
-  uint32_t* part;             // amax partials (31-bit magnitudes), one per CTA, or null
-  int n_part;                 // column kernel: partials to reduce
-  float* amax_out;            // per-tensor recipes: written by CTA 0 of the last kernel
-  float* scale_out;           // tensorwise: written
-  float* scale_inv_out;
-  int margin;
-  int pow2;                   // blockwise: power-of-two scales in the MXFP8 layout
-  int col_bf16;
-  int keep_h;                 // row kernel: h (x without a residual) is read again, from L2
-};
-
-// |a|, |b|, |c|: the largest; NaN if one of them is.
-__device__ __forceinline__ float max3_abs(float a, float b, float c) {
-  float r;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// y of a row's eight columns: (h rstd) gamma, each product rounded.
-__device__ __forceinline__ void norm_row8(uint4 h, float rstd, const float2 (&g)[4],
-                                          float2 (&y)[4]) {
-  const float2 r = make_float2(rstd, rstd);
-  float2 f[4];
-  widen8(h, f);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(__fmul2_rn(f[k], r), g[k]);
-}
-__device__ __forceinline__ float max8_abs(const float2 (&y)[4]) {
-  const float m = max3_abs(max3_abs(y[0].x, y[0].y, y[1].x), y[1].y, y[2].x);
-  return max3_abs(max3_abs(m, y[2].y, y[3].x), y[3].y, 0.0f);
-}
-
-// Largest magnitude over the CTA, in thread 0 (red: one word per warp).
-__device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  const int t = threadIdx.y * blockDim.x + threadIdx.x;
-  __syncthreads();
-  if ((t & 31) == 0) red[t >> 5] = v;
-  __syncthreads();
-  uint32_t m = 0;
-  for (int i = 0; i < int((blockDim.x * blockDim.y) >> 5); ++i) m = max(m, red[i]);
-  return m;
-}
-
 // ------------------------------------------------------------------------- rows
 // tpr threads per row (16, or a multiple of 32), V 16-byte vectors a thread; vector j of lane l
 // holds columns 8 (j tpr + l) .. so a warp reads 512 consecutive bytes and a block of 32 (128)
@@ -104,30 +40,6 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t v, uint32_t* red) {
 // What bounds it: memory with a residual (8192 x 4096, MXFP8 row copy: 236 MB in 37.7 us, 6260
 // GB/s); without one the instructions as much (21.4 us for 15.0 of memory, of which the second sum
 // over the lanes, see there, is 1.2).
-
-// Reduce the V vectors' values over the lanes that differ in the bits OFF .. 1: as long as there
-// is more than one vector, a lane passes on half of them and keeps the half that its bit names.
-// With L = 2 OFF lanes: for V >= L lane l ends with the vectors (V / L) (l % L) .. in m[0] ..,
-// for V < L with vector (l % L) / (L / V) in m[0].
-template <int V, int OFF>
-__device__ __forceinline__ void scatter_max(uint32_t (&m)[V]) {
-  const int lane = threadIdx.x & 31;
-  int n = V;
-#pragma unroll
-  for (int off = OFF; off > 0; off >>= 1) {
-    if (n > 1) {
-      n >>= 1;
-      const bool up = (lane & off) != 0;
-#pragma unroll
-      for (int i = 0; i < V / 2; ++i)
-        if (i < n)
-          m[i] = max(up ? m[i + n] : m[i],
-                     __shfl_xor_sync(0xffffffffu, up ? m[i] : m[i + n], off));
-    } else {
-      m[0] = max(m[0], __shfl_xor_sync(0xffffffffu, m[0], off));
-    }
-  }
-}
 
 // Rows on their way while one is worked on: as many as make four vectors a thread. 131072 x 256
 // (one vector): both MXFP8 copies with a residual 0.67 -> 0.75 of the measured bandwidth, delayed
@@ -285,91 +197,7 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     if (!want_y) continue;
     const float rl = live ? rstd : 0.0f;                         // padding rows: (0 0) gamma = 0
 
-    // ---- the blocks' maxima and multipliers
-    uint32_t m[V];
-    float mult[V];
-    if (OUT == N_MX || OUT == N_BW) {
-#pragma unroll
-      for (int j = 0; j < V; ++j) {
-        float2 y[4];
-        norm_row8(h[j], rl, gamma_of(j), y);
-        m[j] = __float_as_uint(max8_abs(y));
-      }
-    }
-    if constexpr (OUT == N_MX) {
-      constexpr int T = V >= 4 ? V / 4 : 1;                      // blocks that a lane scales
-      scatter_max<V, 2>(m);
-      const int q = lane & 3, s = (lane >> 2) & 3;
-      uint32_t w[T];
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
-        // the four bytes of an atom's row in one word
-        w[t] = mx_scale_byte_f32(m[t], &mult[t]) << (8 * s);
-        w[t] |= __shfl_xor_sync(0xffffffffu, w[t], 4);
-        w[t] |= __shfl_xor_sync(0xffffffffu, w[t], 8);
-      }
-      uint32_t word = w[0];                                      // of the 16 lanes' vector j
-#pragma unroll
-      for (int t = 1; t < T; ++t) word = s == t ? w[t] : word;
-      const int j = V >= 4 ? T * q + s : V == 2 ? q >> 1 : 0, v = j * tpr + (lane & ~15);
-      if (stored && v < nv && (V >= 4 ? s < T : s == 0 && (V == 2 ? (q & 1) == 0 : q == 0)))
-        *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
-                                     mx_scale_offset32(r, v >> 2, p.cols)) = word;
-    }
-    if constexpr (OUT == N_BW) {
-      scatter_max<V, 8>(m);
-      float sinv;
-      mult[0] = scale_from_amax(__uint_as_float(m[0]), p.margin, &sinv, 448.0f, p.pow2);
-      const int j = (lane & 15) / (16 / V), v = j * tpr + (lane & ~15);
-      if (stored && v < nv && (lane & 15) % (16 / V) == 0) {
-        if (p.pow2)
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
-                                       mx_scale_offset32(r, v >> 2, p.cols)) =
-              e8m0_of_pow2(sinv) * 0x01010101u;
-        else
-          reinterpret_cast<float*>(p.row_scale)[int64_t(v >> 4) * p.rows_pad + r] = sinv;
-      }
-    }
-
-    // ---- codes
-    // (a quantised tensor has less than 2^31 elements). Padding rows: (0 0) gamma has gamma's sign,
-    // their codes are +0.
-    const uint32_t kept = live ? 0xffffffffu : 0u;
-    uint8_t* row =
-        OUT == N_STATS ? nullptr : p.row + (uint32_t(r) * uint32_t(p.cols) + uint32_t(8 * lane));
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int v = j * tpr + lane;
-      const bool in = v < nv;                 // uniform over the lanes of a block
-      float2 y[4];
-      // (for the amax, no NaN where a row's rstd is infinite and a lane has no column)
-      const float rj = OUT == N_STATS || OUT == N_TENSOR ? (in ? rl : 0.0f) : rl;
-      norm_row8(h[j], rj, gamma_of(j), y);
-      if (p.y != nullptr && live && in)
-        *reinterpret_cast<uint4*>(p.y + r * p.cols + 8 * v) =
-            make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y),
-                       pack_bf16(y[2].x, y[2].y), pack_bf16(y[3].x, y[3].y));
-      if constexpr (OUT == N_STATS || OUT == N_TENSOR)
-        amax = max(amax, __float_as_uint(max8_abs(y)));
-      if constexpr (OUT != N_STATS) {
-        float s = tensor_scale;
-        if constexpr (OUT == N_MX) {
-          constexpr int T = V >= 4 ? V / 4 : 1;
-          s = __shfl_sync(0xffffffffu, mult[j % T],
-                          (wl & 28) | (V >= 4 ? j / T : V == 2 ? 2 * j : 0));
-        }
-        if constexpr (OUT == N_BW)
-          s = __shfl_sync(0xffffffffu, mult[0], (wl & 16) | (j * (16 / V)));
-        const float2 s2 = make_float2(s, s);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(y[k], s2);
-        if (in && stored)
-          stg_v2_policy(row + 8 * j * tpr,
-                        make_uint2(cvt_e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y) & kept,
-                                   cvt_e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y) & kept),
-                        codes);
-      }
-    }
+    norm_row_copy<V, OUT>(p, h, rl, gamma_of, r, live, stored, lane, tensor_scale, codes, amax);
   }
   if constexpr (OUT == N_STATS || OUT == N_TENSOR) {
     if (p.part != nullptr) {
@@ -663,8 +491,6 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
 
 namespace {
 
-constexpr int kNormMaxParts = 4096;   // amax partials: one per CTA of the row kernel
-
 // Vectors a thread: enough loads in flight, but no more registers than that needs. With a residual
 // (twice the loads) two, 4096 columns then being 256 threads (8192 x 4096, row copy: 37.7 us; four
 // 39.2, one 47.1); without one four (both copies: 33.6; two 36.9); and four for longer rows, of
@@ -714,6 +540,13 @@ cudaError_t launch_rows(const NormParams& p, int* ctas, cudaStream_t st) {
                           : launch_rows<OUT, false>(p, ctas, st);
 }
 
+cudaError_t norm_rows(int out_kind, const NormParams& p, const void*, int* ctas, cudaStream_t st) {
+  return out_kind == N_MX       ? launch_rows<N_MX>(p, ctas, st)
+         : out_kind == N_BW     ? launch_rows<N_BW>(p, ctas, st)
+         : out_kind == N_TENSOR ? launch_rows<N_TENSOR>(p, ctas, st)
+                                : launch_rows<N_STATS>(p, ctas, st);
+}
+
 template <int OUT>
 cudaError_t launch_cols(const NormParams& p, cudaStream_t st) {
   const int tiles_c = (p.cols + 63) / 64;
@@ -742,8 +575,7 @@ size_t norm_workspace_bytes(int kind, int64_t rows, int64_t cols) {
   return size_t((rows * 4 + 15) / 16 * 16) + (tensor ? size_t(kNormMaxParts) * 4 : 0);
 }
 
-cudaError_t norm_quantize_launch(const NormArgs& a, fp8_tensor* out, void* workspace,
-                                 cudaStream_t st) {
+NormParams norm_params(const NormArgs& a) {
   NormParams p{};
   p.x = a.x;
   p.res = a.res;
@@ -762,7 +594,12 @@ cudaError_t norm_quantize_launch(const NormArgs& a, fp8_tensor* out, void* works
   p.margin = a.margin;
   p.pow2 = a.pow2;
   p.col_bf16 = a.col_bf16;
-  if (!a.quantise) return launch_rows<N_STATS>(p, nullptr, st);
+  return p;
+}
+
+cudaError_t norm_copies_launch(const NormArgs& a, NormParams p, fp8_tensor* out, void* workspace,
+                               cudaStream_t st, NormRowLaunch rows, const void* more) {
+  if (!a.quantise) return rows(N_STATS, p, more, nullptr, st);
 
   uint32_t* part = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(workspace) +
                                                (a.rows * 4 + 15) / 16 * 16);
@@ -784,11 +621,8 @@ cudaError_t norm_quantize_launch(const NormArgs& a, fp8_tensor* out, void* works
     if (!tensorwise) p.scale_in = out->scale;
   }
   int ctas = 0;
-  cudaError_t e;
-  if (p.row == nullptr || tensorwise) e = launch_rows<N_STATS>(p, &ctas, st);
-  else if (out_kind == N_MX) e = launch_rows<N_MX>(p, &ctas, st);
-  else if (out_kind == N_BW) e = launch_rows<N_BW>(p, &ctas, st);
-  else e = launch_rows<N_TENSOR>(p, &ctas, st);
+  const cudaError_t e =
+      rows(p.row == nullptr || tensorwise ? int(N_STATS) : out_kind, p, more, &ctas, st);
   if (e != cudaSuccess) return e;
   if (!cols) {
     if (out_kind != N_TENSOR) return cudaSuccess;
@@ -807,6 +641,11 @@ cudaError_t norm_quantize_launch(const NormArgs& a, fp8_tensor* out, void* works
   p.scale_inv_out = out->scale_inv;
   if (!tensorwise) p.row = nullptr;                           // the row kernel wrote it
   return launch_cols<N_TENSOR>(p, st);
+}
+
+cudaError_t norm_quantize_launch(const NormArgs& a, fp8_tensor* out, void* workspace,
+                                 cudaStream_t st) {
+  return norm_copies_launch(a, norm_params(a), out, workspace, st, norm_rows, nullptr);
 }
 
 }  // namespace fp8lin
