@@ -548,6 +548,87 @@ fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe *recipe, const fp8_branc
                                        cudaStream_t stream);
 
 /*
+ * fp8_checkpoint_quantize — the FP8 copies of the linear layer's X made (again) from a checkpoint,
+ * so that a training step need not keep them: above all the column copy, which only the backward
+ * pass reads.
+ *   y = (h * rstd) * gamma       the norm's output, from the stream's checkpoint and the forward
+ *                                pass's rstd; or y = h with rstd and gamma both NULL
+ * with h the checkpoint's values: a copy made from them is that of the 8-bit h, not of the bf16 one.
+ *   in        checkpoint of [rows][cols]
+ *   rstd      [rows] fp32, gamma [cols] (gamma_fp32 0: bf16, 1: fp32): both or neither
+ *   recipe, want_row, want_col, out, workspace (fp8_rmsnorm_workspace_bytes), shapes and padding:
+ *             as for fp8_rmsnorm_quantize; one copy at least. A block that reads back as NaN gives
+ *             codes 0x7F.
+ */
+fp8_status fp8_checkpoint_quantize(const fp8_recipe *recipe, const fp8_checkpoint *in,
+                                   int64_t rows, int64_t cols, const float *rstd,
+                                   const void *gamma, int32_t gamma_fp32, int32_t want_row,
+                                   int32_t want_col, fp8_tensor *out, void *workspace,
+                                   size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/* fp8_rmsnorm_bwd_checkpoint — fp8_rmsnorm_bwd with h read from its checkpoint (in->h and in->ld_h
+ * are not looked at): half of h's memory and a seventh of the call's traffic less. Workspace as for
+ * fp8_rmsnorm_bwd. A block whose byte is 0xFF makes its row of dh and its columns of dgamma NaN. */
+fp8_status fp8_rmsnorm_bwd_checkpoint(const fp8_norm_grad *in, const fp8_checkpoint *h_ckpt,
+                                      void *dh_bf16, float *dgamma, void *workspace,
+                                      size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
+
+/* Inputs of fp8_branch_rmsnorm_quantize's backward pass; pointers and pitches as there. */
+typedef struct {
+  const void *dy;            /* [rows][cols] bf16: the gradient of y */
+  const void *dres;          /* [rows][cols] bf16: the gradient of h on the residual path, or NULL */
+  const void *h;             /* [rows][cols] bf16: the stream that the norm read; not looked at with
+                                h_ckpt */
+  const void *branch;        /* [rows][cols] bf16; not looked at with branch_ckpt */
+  fp8_checkpoint h_ckpt, branch_ckpt;   /* checkpoints to read instead; codes NULL: none */
+  const void *gamma_post, *gate;        /* as in the forward pass */
+  const float *token_gate;
+  const void *gamma;
+  const float *rstd_branch;  /* [rows], with gamma_post: as the forward pass wrote them */
+  const float *rstd;         /* [rows] */
+  int64_t ld_dy, ld_dres, ld_h, ld_branch;
+  int64_t rows, cols;
+  int32_t gamma_post_fp32, gate_fp32, gamma_fp32;
+  float scale;
+} fp8_branch_grad;
+
+/* Its outputs. The vectors are fp32, overwritten (the columns' zeros when rows is 0), 16-byte
+ * aligned (dtoken_gate 4-byte); each may be NULL. */
+typedef struct {
+  void *dh;                  /* [rows][cols] bf16, contiguous: the gradient of residual */
+  void *dbranch;             /* [rows][cols] bf16, contiguous */
+  float *dgamma;             /* [cols] */
+  float *dgamma_post;        /* [cols]; NULL without gamma_post */
+  float *dgate;              /* [cols]; NULL without gate */
+  float *dtoken_gate;        /* [rows]; NULL without token_gate */
+} fp8_branch_grad_out;
+
+/* Bytes of scratch fp8_branch_rmsnorm_bwd needs (0 when none of dgamma, dgamma_post and dgate is
+ * wanted). */
+size_t fp8_branch_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * fp8_branch_rmsnorm_bwd — backward of fp8_branch_rmsnorm_quantize, in fp32:
+ *   xh = h * rstd,  a = dy * gamma
+ *   dh = dres + rstd * (a - xh * mean_c(a * xh))        the gradient of h and of residual alike
+ *   u = dh * w,  s[r] = sum_c u * xo                     (xo, w: as in the forward pass)
+ *   dbranch = rstd_branch * token_gate * (u - xo * s / cols)   (token_gate * u without gamma_post)
+ *   dgamma = sum_r dy * xh,  S[c] = sum_r token_gate * dh * xo
+ *   dgamma_post = scale * gate * S,  dgate = scale * gamma_post * S,  dtoken_gate[r] = s[r]
+ * dbranch and the sums follow from dh before its rounding to bf16. A token whose gate is 0 has a
+ * dbranch of zeros and adds nothing to S, whatever its row of branch holds; its dtoken_gate is s,
+ * of that row.
+ *   dh, dbranch   each may be one of dy, dres, h and branch itself when that is contiguous (not
+ *                 both the same).
+ *   workspace     fp8_branch_rmsnorm_bwd_workspace_bytes() of device scratch.
+ * Equal calls give equal bits (a fixed order of additions, which follows from the numbers of rows
+ * and columns). rows >= 0; cols a multiple of 16, at most 32768. dev_status is not written.
+ */
+fp8_status fp8_branch_rmsnorm_bwd(const fp8_branch_grad *in, const fp8_branch_grad_out *out,
+                                  void *workspace, size_t ws_bytes, int32_t *dev_status,
+                                  cudaStream_t stream);
+
+/*
  * The gradients of a step, before the optimizer: their global norm and clipping by it.
  *   norm = scale * sqrt(sum over all tensors of g^2)
  *   coef = scale * min(1, max_norm / (norm + 1e-6))

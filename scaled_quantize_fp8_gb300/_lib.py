@@ -84,6 +84,26 @@ class BranchInput(ctypes.Structure):
                 ("eps_post", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class BranchGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("dres", ctypes.c_void_p), ("h", ctypes.c_void_p),
+                ("branch", ctypes.c_void_p), ("h_ckpt", Checkpoint),
+                ("branch_ckpt", Checkpoint), ("gamma_post", ctypes.c_void_p),
+                ("gate", ctypes.c_void_p), ("token_gate", ctypes.c_void_p),
+                ("gamma", ctypes.c_void_p), ("rstd_branch", ctypes.c_void_p),
+                ("rstd", ctypes.c_void_p), ("ld_dy", ctypes.c_int64),
+                ("ld_dres", ctypes.c_int64), ("ld_h", ctypes.c_int64),
+                ("ld_branch", ctypes.c_int64), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("gamma_post_fp32", ctypes.c_int32),
+                ("gate_fp32", ctypes.c_int32), ("gamma_fp32", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class BranchGradOut(ctypes.Structure):
+    _fields_ = [("dh", ctypes.c_void_p), ("dbranch", ctypes.c_void_p),
+                ("dgamma", ctypes.c_void_p), ("dgamma_post", ctypes.c_void_p),
+                ("dgate", ctypes.c_void_p), ("dtoken_gate", ctypes.c_void_p)]
+
+
 # The norms' inputs, the clip rule and the norm's recipe as bytes: the binding builds one per call, which
 # takes half the time of a Structure. The functions take either (their argument is a c_void_p).
 pack_recipe = struct.Struct("@iiiiiii").pack
@@ -91,6 +111,8 @@ pack_norm_input = struct.Struct("@PPPqqqqif").pack
 pack_norm_grad = struct.Struct("@PPPPPqqqqqi4x").pack
 pack_checkpoint = struct.Struct("@PP").pack
 pack_branch_input = struct.Struct("@PPPPPPqqqqiiifff").pack
+pack_branch_grad = struct.Struct("@14P6qiiif").pack
+pack_branch_grad_out = struct.Struct("@6P").pack
 pack_clip_rule = struct.Struct("@ff").pack
 
 GRAD_BF16, GRAD_FP32 = 0, 1
@@ -151,6 +173,11 @@ _SIG = {
     "fp8_checkpoint_scale_bytes": (ctypes.c_size_t, [_I64, _I64]),
     "fp8_checkpoint_write": (_I32, [_P, _I64, _I64, _I64, _P, _P]),
     "fp8_checkpoint_read": (_I32, [_P, _I64, _I64, _P, _P]),
+    "fp8_checkpoint_quantize": (_I32, [_P, _P, _I64, _I64, _P, _P, _I32, _I32, _I32,
+                                       ctypes.POINTER(Tensor), _P, ctypes.c_size_t, _P, _P]),
+    "fp8_rmsnorm_bwd_checkpoint": (_I32, [_P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]),
+    "fp8_branch_rmsnorm_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "fp8_branch_rmsnorm_bwd": (_I32, [_P, _P, _P, ctypes.c_size_t, _P, _P]),
     "fp8_branch_rmsnorm_quantize": (_I32, [_P, _P, _I32, _I32, _P, _P, _P, _P, _P, _P,
                                            ctypes.POINTER(Tensor), _P, ctypes.c_size_t, _P, _P]),
     "fp8_grad_workspace_bytes": (ctypes.c_size_t, [_I32]),

@@ -7,7 +7,7 @@ built on demand.
 """
 import ctypes
 from dataclasses import dataclass, field
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -573,12 +573,13 @@ def rmsnorm_bwd_workspace_bytes(rows, cols):
     return int(L.load().fp8_rmsnorm_bwd_workspace_bytes(rows, cols))
 
 
-def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: torch.Tensor,
+def rmsnorm_bwd(dy: torch.Tensor, h: "torch.Tensor | Checkpoint", rstd: torch.Tensor, gamma: torch.Tensor,
                 dres: Optional[torch.Tensor] = None, want_dgamma=True,
                 dh: Optional[torch.Tensor] = None, dgamma: Optional[torch.Tensor] = None,
                 workspace: Optional[torch.Tensor] = None, status=None, stream=None):
-    """fp8_rmsnorm_bwd: the gradient of the residual stream (of x and residual alike, `dres` the
-    gradient that reaches it past the norm) and of gamma. rstd's length is the number of rows;
+    """fp8_rmsnorm_bwd (fp8_rmsnorm_bwd_checkpoint where h is a Checkpoint): the gradient of the
+    residual stream (of x and residual alike, `dres` the gradient that reaches it past the norm) and
+    of gamma. rstd's length is the number of rows;
     dy may have more (linear_bwd's dx of the padded tensor): the rest is not read. Returns
     (dh, dgamma)."""
     lib = L.load()
@@ -594,8 +595,15 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
         if dres.shape != shape:
             raise ValueError("dres: the shape of h")
         ld_dres, dres_ptr = _rows_2d(dres, cols, "dres"), dres.data_ptr()
+    ck = None
+    if type(h) is Checkpoint:
+        ck = _checkpoint(h, shape, "h")
+        _one_device(dy, h.codes, h.scale, rstd, gamma, dres, dh, dgamma, workspace)
+        h, ld_h = h.codes, cols
+    else:
+        ld_h = _rows_2d(h, cols, "h")
     inp = L.pack_norm_grad(dy.data_ptr(), h.data_ptr(), dres_ptr, gamma.data_ptr(),
-                           rstd.data_ptr(), _rows_2d(dy, cols, "dy"), _rows_2d(h, cols, "h"),
+                           rstd.data_ptr(), _rows_2d(dy, cols, "dy"), ld_h,
                            ld_dres, rows, cols, _gamma(gamma, cols))
     if dh is None:
         dh = _empty(shape, _BF16, h.device, stream)
@@ -612,15 +620,20 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor, gamma: to
             and (dres is None or dres.is_cuda) and (dgamma is None or dgamma.is_cuda)
             and (workspace is None or workspace.is_cuda)):
         _not_on_gpu()
-    args = (inp, dh.data_ptr(), None if dgamma is None else dgamma.data_ptr())
+    args = (dh.data_ptr(), None if dgamma is None else dgamma.data_ptr())
     rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
-    st = lib.fp8_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
+    if ck is None:
+        call, args, name = lib.fp8_rmsnorm_bwd, (inp, *args), "fp8_rmsnorm_bwd"
+    else:
+        call, args = lib.fp8_rmsnorm_bwd_checkpoint, (inp, ck, *args)
+        name = "fp8_rmsnorm_bwd_checkpoint"
+    st = call(*args, *_buffer(workspace), *rest)
     if st == L.FP8_ERR_WORKSPACE:
         workspace = _empty(lib.fp8_rmsnorm_bwd_workspace_bytes(rows, cols), torch.uint8, h.device,
                            stream)
-        st = lib.fp8_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
+        st = call(*args, *_buffer(workspace), *rest)
     if st:
-        L.check(st, "fp8_rmsnorm_bwd")
+        L.check(st, name)
     return dh, dgamma
 
 
@@ -815,6 +828,169 @@ def branch_rmsnorm_quantize(recipe: Optional[Recipe], branch: torch.Tensor,
         out.rows, out.cols, out.kind, out.role = padded, cols, fields[0], L.ROLE_ACTIVATION
         out.col_bf16 = 1 - fields[5]                       # as the library sets them
     return out, h, rstd, rstd_branch, y
+
+
+def checkpoint_quantize(recipe: Recipe, ck: Checkpoint, rstd: Optional[torch.Tensor] = None,
+                        gamma: Optional[torch.Tensor] = None, want_row=True, want_col=True,
+                        out: Optional[QTensor] = None, workspace: Optional[torch.Tensor] = None,
+                        status=None, stream=None):
+    """fp8_checkpoint_quantize: the FP8 copies of a checkpointed activation, or with rstd and gamma
+    of its RMSNorm, padded with rows of zeros to the recipe's row quantum as rmsnorm_quantize's. A
+    training step that keeps the checkpoint need not keep the column copy that wgrad reads. `out`,
+    workspace (rmsnorm_workspace_bytes) and delayed scaling as for rmsnorm_quantize."""
+    lib = L.load()
+    shape = ck.codes.shape
+    if len(shape) != 2:
+        raise TypeError("codes: a [rows, cols] tensor")
+    rows, cols = shape
+    c = _checkpoint(ck, shape, "ck")
+    if (rstd is None) != (gamma is None):
+        raise ValueError("rstd and gamma: both or neither")
+    gamma_fp32 = 0
+    if rstd is not None:
+        _like(rstd, (rows,), _FP32, "rstd")
+        gamma_fp32 = _gamma(gamma, cols)
+    _one_device(ck.codes, ck.scale, rstd, gamma, workspace)
+    block = recipe.kind in ("mxfp8", "blockwise")
+    q = 128 if block else 16
+    padded = -(-rows // q) * q
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
+                                device=ck.codes.device)
+    ct, on_gpu = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
+    if not on_gpu:
+        _not_on_gpu()
+    fields = recipe._fields()
+    rc = L.pack_recipe(*fields)
+    args = (rc, c, rows, cols, None if rstd is None else rstd.data_ptr(),
+            None if gamma is None else gamma.data_ptr(), gamma_fp32, want_row, want_col,
+            ctypes.byref(ct))
+    rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
+    st = lib.fp8_checkpoint_quantize(*args, *_buffer(workspace), *rest)
+    if st == L.FP8_ERR_WORKSPACE:
+        workspace = _empty(lib.fp8_rmsnorm_workspace_bytes(rc, rows, cols), torch.uint8,
+                           ck.codes.device, stream)
+        st = lib.fp8_checkpoint_quantize(*args, *_buffer(workspace), *rest)
+    if st:
+        L.check(st, "fp8_checkpoint_quantize")
+    out.rows, out.cols, out.kind, out.role = padded, cols, fields[0], L.ROLE_ACTIVATION
+    out.col_bf16 = 1 - fields[5]
+    return out
+
+
+class BranchGrads(NamedTuple):
+    """What branch_rmsnorm_bwd returns; None where there is nothing to derive by, or none wanted."""
+    dh: torch.Tensor                        # of residual
+    dbranch: torch.Tensor
+    dgamma: Optional[torch.Tensor]
+    dgamma_post: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dtoken_gate: Optional[torch.Tensor]
+
+
+def branch_rmsnorm_bwd_workspace_bytes(rows, cols):
+    return int(L.load().fp8_branch_rmsnorm_bwd_workspace_bytes(rows, cols))
+
+
+def branch_rmsnorm_bwd(dy: torch.Tensor, h: "torch.Tensor | Checkpoint", rstd: torch.Tensor,
+                       gamma: torch.Tensor, branch: "torch.Tensor | Checkpoint",
+                       rstd_branch: Optional[torch.Tensor] = None,
+                       gamma_post: Optional[torch.Tensor] = None,
+                       gate: Optional[torch.Tensor] = None,
+                       token_gate: Optional[torch.Tensor] = None, scale=1.0,
+                       dres: Optional[torch.Tensor] = None, want_dgamma=True,
+                       dh: Optional[torch.Tensor] = None,
+                       dbranch: Optional[torch.Tensor] = None,
+                       dgamma: Optional[torch.Tensor] = None,
+                       dgamma_post: Optional[torch.Tensor] = None,
+                       dgate: Optional[torch.Tensor] = None,
+                       dtoken_gate: Optional[torch.Tensor] = None,
+                       workspace: Optional[torch.Tensor] = None, status=None, stream=None):
+    """fp8_branch_rmsnorm_bwd: the gradients of branch_rmsnorm_quantize's inputs from dy, that of its
+    output (it may have more rows than rstd has entries, as linear_bwd's dx of the padded tensor:
+    the rest is not read), and dres, the gradient that reaches h past the norm. h and branch, each
+    a bf16 tensor or its Checkpoint, rstd, rstd_branch and the weights are those of the forward
+    pass. Returns BranchGrads; want_dgamma False leaves out the gradients per channel (dgamma,
+    dgamma_post, dgate)."""
+    lib = L.load()
+    shape = h.shape
+    if len(shape) != 2 or dy.dim() != 2:
+        raise TypeError("dy, h: [rows, cols] tensors")
+    rows, cols = shape
+    if dy.shape[0] < rows or dy.shape[1] != cols:
+        raise ValueError("dy, h: [rows, cols] with one row per entry of rstd")
+    if branch.shape != shape:
+        raise ValueError("branch: the shape of h")
+    _like(rstd, (rows,), _FP32, "rstd")
+    tensors = [dy, rstd, gamma, gamma_post, gate, token_gate, dres, workspace]
+    none = (0, 0)
+    h_ptr = o_ptr = ld_h = ld_o = 0
+    h_ck = o_ck = none
+    if type(h) is Checkpoint:
+        _checkpoint(h, shape, "h")
+        h_ck = (h.codes.data_ptr(), h.scale.data_ptr())
+        tensors += (h.codes, h.scale)
+    else:
+        h_ptr, ld_h = h.data_ptr(), _rows_2d(h, cols, "h")
+        tensors.append(h)
+    if type(branch) is Checkpoint:
+        _checkpoint(branch, shape, "branch")
+        o_ck = (branch.codes.data_ptr(), branch.scale.data_ptr())
+        tensors += (branch.codes, branch.scale)
+    else:
+        o_ptr, ld_o = branch.data_ptr(), _rows_2d(branch, cols, "branch")
+        tensors.append(branch)
+    post_ptr, post_fp32 = _columns(gamma_post, cols, "gamma_post")
+    gate_ptr, gate_fp32 = _columns(gate, cols, "gate")
+    ro_ptr = token_ptr = 0
+    if gamma_post is not None:
+        if rstd_branch is None:
+            raise ValueError("rstd_branch: the forward pass's, with gamma_post")
+        _like(rstd_branch, (rows,), _FP32, "rstd_branch")
+        tensors.append(rstd_branch)
+        ro_ptr = rstd_branch.data_ptr()
+    if token_gate is not None:
+        _like(token_gate, (rows,), _FP32, "token_gate")
+        token_ptr = token_gate.data_ptr()
+    ld_dres = dres_ptr = 0
+    if dres is not None:
+        if dres.shape != shape:
+            raise ValueError("dres: the shape of h")
+        ld_dres, dres_ptr = _rows_2d(dres, cols, "dres"), dres.data_ptr()
+    inp = L.pack_branch_grad(dy.data_ptr(), dres_ptr, h_ptr, o_ptr, *h_ck, *o_ck, post_ptr,
+                             gate_ptr, token_ptr, gamma.data_ptr(), ro_ptr, rstd.data_ptr(),
+                             _rows_2d(dy, cols, "dy"), ld_dres, ld_h, ld_o, rows, cols, post_fp32,
+                             gate_fp32, _gamma(gamma, cols), scale)
+    device = dy.device
+
+    def made(t, shape, dtype, name, wanted=True):
+        if not wanted:
+            return None
+        if t is None:
+            t = _empty(shape, dtype, device, stream)
+        else:
+            _like(t, shape, dtype, name)
+        tensors.append(t)
+        return t
+
+    out = BranchGrads(
+        made(dh, shape, _BF16, "dh"), made(dbranch, shape, _BF16, "dbranch"),
+        made(dgamma, (cols,), _FP32, "dgamma", want_dgamma),
+        made(dgamma_post, (cols,), _FP32, "dgamma_post", want_dgamma and gamma_post is not None),
+        made(dgate, (cols,), _FP32, "dgate", want_dgamma and gate is not None),
+        made(dtoken_gate, (rows,), _FP32, "dtoken_gate", token_gate is not None))
+    _one_device(*tensors)
+    args = (inp, L.pack_branch_grad_out(*[0 if t is None else t.data_ptr() for t in out]))
+    rest = (None if status is None else status.data_ptr(), _raw_stream(stream))
+    st = lib.fp8_branch_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
+    if st == L.FP8_ERR_WORKSPACE:
+        workspace = _empty(lib.fp8_branch_rmsnorm_bwd_workspace_bytes(rows, cols), torch.uint8,
+                           device, stream)
+        st = lib.fp8_branch_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
+    if st:
+        L.check(st, "fp8_branch_rmsnorm_bwd")
+    return out
 
 
 _GRAD_DTYPES = {torch.bfloat16: L.GRAD_BF16, torch.float32: L.GRAD_FP32}

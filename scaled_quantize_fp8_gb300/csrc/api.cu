@@ -616,9 +616,10 @@ fp8_status check_norm_shape(int64_t rows, int64_t cols, int64_t quantum) {
 }
 
 // The checks of a call that normalises rows into copies: `a` holds the inputs and outputs; what the
-// recipe says is filled in.
+// recipe says is filled in. from_x: x and gamma are inputs of the call.
 fp8_status check_norm(const fp8_recipe* recipe, int32_t want_row, int32_t want_col,
-                      const fp8_tensor* out, NormArgs* a, const void* workspace, size_t ws_bytes) {
+                      const fp8_tensor* out, NormArgs* a, const void* workspace, size_t ws_bytes,
+                      bool from_x = true) {
   a->quantise = want_row || want_col;
   if (a->quantise) {
     FP8_TRY(check_recipe(recipe));
@@ -640,9 +641,11 @@ fp8_status check_norm(const fp8_recipe* recipe, int32_t want_row, int32_t want_c
   if (a->gamma_fp32 != 0 && a->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
   if (a->quantise) FP8_TRY(check_scalars(a->kind, out));
   if (rows == 0 || cols == 0) return FP8_OK;
-  FP8_TRY(check_ptr(a->x));
-  FP8_TRY(check_pitch(a->ldx, cols));
-  FP8_TRY(check_ptr(a->gamma));
+  if (from_x) {
+    FP8_TRY(check_ptr(a->x));
+    FP8_TRY(check_pitch(a->ldx, cols));
+    FP8_TRY(check_ptr(a->gamma));
+  }
   if (a->res != nullptr) {
     FP8_TRY(check_ptr(a->res));
     FP8_TRY(check_pitch(a->ldr, cols));
@@ -700,6 +703,51 @@ fp8_status check_checkpoint_shape(int64_t rows, int64_t cols) {
   if (rows < 0 || cols < 0 || cols % 16 != 0 || cols > kCheckpointMaxCols) return FP8_ERR_SHAPE;
   if (cols > 0 && rows > (int64_t(1) << 40) / cols) return FP8_ERR_SHAPE;
   return FP8_OK;
+}
+
+fp8_status norm_bwd(const fp8_norm_grad* in, const fp8_checkpoint* h_ckpt, void* dh_bf16,
+                    float* dgamma, void* workspace, size_t ws_bytes, cudaStream_t stream) {
+  if (in == nullptr) return FP8_ERR_NULL;
+  const int64_t rows = in->rows, cols = in->cols;
+  FP8_TRY(check_norm_shape(rows, cols, 16));
+  if (in->gamma_fp32 != 0 && in->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
+  if (dgamma != nullptr && !aligned16(dgamma)) return FP8_ERR_ALIGN;
+  if (cols == 0) return FP8_OK;
+  if (rows == 0)
+    return dgamma == nullptr ? FP8_OK
+                             : cuda_status(cudaMemsetAsync(dgamma, 0, size_t(cols) * 4, stream));
+  FP8_TRY(check_ptr(in->dy));
+  FP8_TRY(check_pitch(in->ld_dy, cols));
+  if (h_ckpt != nullptr) {
+    FP8_TRY(check_checkpoint(h_ckpt));
+  } else {
+    FP8_TRY(check_ptr(in->h));
+    FP8_TRY(check_pitch(in->ld_h, cols));
+  }
+  FP8_TRY(check_ptr(in->gamma));
+  if (in->rstd == nullptr) return FP8_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(in->rstd) % 4 != 0) return FP8_ERR_ALIGN;
+  if (in->dres != nullptr) {
+    FP8_TRY(check_ptr(in->dres));
+    FP8_TRY(check_pitch(in->ld_dres, cols));
+  }
+  FP8_TRY(check_ptr(dh_bf16));
+  if ((dh_bf16 == in->dy && in->ld_dy != cols) || (dh_bf16 == in->dres && in->ld_dres != cols))
+    return FP8_ERR_SHAPE;                   // in place only where dh's rows lie on the input's
+  const size_t need = dgamma == nullptr ? 0 : norm_bwd_workspace_bytes(rows, cols);
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
+  return cuda_status(norm_bwd_launch(*in, h_ckpt, reinterpret_cast<uint16_t*>(dh_bf16), dgamma,
+                                     workspace, stream));
+}
+
+fp8_status check_rows(const void* p, int64_t ld, int64_t cols) {
+  FP8_TRY(check_ptr(p));
+  return check_pitch(ld, cols);
+}
+
+fp8_status check_floats(const float* p) {
+  return reinterpret_cast<uintptr_t>(p) % 4 != 0 ? FP8_ERR_ALIGN : FP8_OK;
 }
 
 fp8_status check_grads(int32_t n, const fp8_grad_item* items, bool outs) {
@@ -766,34 +814,15 @@ size_t fp8_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
 fp8_status fp8_rmsnorm_bwd(const fp8_norm_grad* in, void* dh_bf16, float* dgamma, void* workspace,
                            size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
   (void)dev_status;                         // no device-side waits in this path
-  if (in == nullptr) return FP8_ERR_NULL;
-  const int64_t rows = in->rows, cols = in->cols;
-  FP8_TRY(check_norm_shape(rows, cols, 16));
-  if (in->gamma_fp32 != 0 && in->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
-  if (dgamma != nullptr && !aligned16(dgamma)) return FP8_ERR_ALIGN;
-  if (cols == 0) return FP8_OK;
-  if (rows == 0)
-    return dgamma == nullptr ? FP8_OK
-                             : cuda_status(cudaMemsetAsync(dgamma, 0, size_t(cols) * 4, stream));
-  FP8_TRY(check_ptr(in->dy));
-  FP8_TRY(check_pitch(in->ld_dy, cols));
-  FP8_TRY(check_ptr(in->h));
-  FP8_TRY(check_pitch(in->ld_h, cols));
-  FP8_TRY(check_ptr(in->gamma));
-  if (in->rstd == nullptr) return FP8_ERR_NULL;
-  if (reinterpret_cast<uintptr_t>(in->rstd) % 4 != 0) return FP8_ERR_ALIGN;
-  if (in->dres != nullptr) {
-    FP8_TRY(check_ptr(in->dres));
-    FP8_TRY(check_pitch(in->ld_dres, cols));
-  }
-  FP8_TRY(check_ptr(dh_bf16));
-  if ((dh_bf16 == in->dy && in->ld_dy != cols) || (dh_bf16 == in->dres && in->ld_dres != cols))
-    return FP8_ERR_SHAPE;                   // in place only where dh's rows lie on the input's
-  const size_t need = dgamma == nullptr ? 0 : norm_bwd_workspace_bytes(rows, cols);
-  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8_ERR_WORKSPACE;
-  if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
-  return cuda_status(norm_bwd_launch(*in, reinterpret_cast<uint16_t*>(dh_bf16), dgamma, workspace,
-                                     stream));
+  return norm_bwd(in, nullptr, dh_bf16, dgamma, workspace, ws_bytes, stream);
+}
+
+fp8_status fp8_rmsnorm_bwd_checkpoint(const fp8_norm_grad* in, const fp8_checkpoint* h_ckpt,
+                                      void* dh_bf16, float* dgamma, void* workspace,
+                                      size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  (void)dev_status;
+  if (h_ckpt == nullptr) return FP8_ERR_NULL;
+  return norm_bwd(in, h_ckpt, dh_bf16, dgamma, workspace, ws_bytes, stream);
 }
 
 size_t fp8_grad_workspace_bytes(int32_t n) { return grad_workspace_bytes(n); }
@@ -889,6 +918,93 @@ fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_branc
   if (empty) return empty_norm(a, want_row, want_col, out, workspace, stream);
   return cuda_status(branch_quantize_launch(a, *in, rstd_branch, branch_ckpt, h_ckpt, out,
                                             workspace, stream));
+}
+
+size_t fp8_branch_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
+  return branch_bwd_workspace_bytes(rows, cols);
+}
+
+fp8_status fp8_branch_rmsnorm_bwd(const fp8_branch_grad* in, const fp8_branch_grad_out* out,
+                                  void* workspace, size_t ws_bytes, int32_t* dev_status,
+                                  cudaStream_t stream) {
+  (void)dev_status;                         // no device-side waits in this path
+  if (in == nullptr || out == nullptr) return FP8_ERR_NULL;
+  const int64_t rows = in->rows, cols = in->cols;
+  FP8_TRY(check_norm_shape(rows, cols, 16));
+  if (in->gamma_fp32 != 0 && in->gamma_fp32 != 1) return FP8_ERR_UNSUPPORTED;
+  FP8_TRY(check_vector(in->gamma_post, in->gamma_post_fp32));
+  FP8_TRY(check_vector(in->gate, in->gate_fp32));
+  if (!finite(in->scale)) return FP8_ERR_UNSUPPORTED;
+  if ((out->dgamma_post != nullptr && in->gamma_post == nullptr) ||
+      (out->dgate != nullptr && in->gate == nullptr) ||
+      (out->dtoken_gate != nullptr && in->token_gate == nullptr))
+    return FP8_ERR_NULL;                    // a gradient of what is not there
+  float* const sums[3] = {out->dgamma, out->dgamma_post, out->dgate};
+  bool want_sums = false;
+  for (float* s : sums) {
+    if (!aligned16(s)) return FP8_ERR_ALIGN;
+    want_sums |= s != nullptr;
+  }
+  FP8_TRY(check_floats(out->dtoken_gate));
+  if (cols == 0) return FP8_OK;
+  if (rows == 0) {
+    for (float* s : sums) {
+      if (s == nullptr) continue;
+      FP8_TRY(cuda_status(cudaMemsetAsync(s, 0, size_t(cols) * 4, stream)));
+    }
+    return FP8_OK;
+  }
+  FP8_TRY(check_rows(in->dy, in->ld_dy, cols));
+  if (in->dres != nullptr) FP8_TRY(check_rows(in->dres, in->ld_dres, cols));
+  const bool h_ckpt = in->h_ckpt.codes != nullptr, branch_ckpt = in->branch_ckpt.codes != nullptr;
+  FP8_TRY(h_ckpt ? check_checkpoint(&in->h_ckpt) : check_rows(in->h, in->ld_h, cols));
+  FP8_TRY(branch_ckpt ? check_checkpoint(&in->branch_ckpt)
+                      : check_rows(in->branch, in->ld_branch, cols));
+  FP8_TRY(check_ptr(in->gamma));
+  if (in->rstd == nullptr || (in->gamma_post != nullptr && in->rstd_branch == nullptr))
+    return FP8_ERR_NULL;
+  FP8_TRY(check_floats(in->rstd));
+  FP8_TRY(check_floats(in->rstd_branch));
+  FP8_TRY(check_floats(in->token_gate));
+  FP8_TRY(check_ptr(out->dh));
+  FP8_TRY(check_ptr(out->dbranch));
+  if (out->dh == out->dbranch) return FP8_ERR_SHAPE;
+  for (const void* d : {out->dh, out->dbranch}) {     // in place only where the rows lie alike
+    if ((d == in->dy && in->ld_dy != cols) || (d == in->dres && in->ld_dres != cols) ||
+        (!h_ckpt && d == in->h && in->ld_h != cols) ||
+        (!branch_ckpt && d == in->branch && in->ld_branch != cols))
+      return FP8_ERR_SHAPE;
+  }
+  const size_t need = want_sums ? branch_bwd_workspace_bytes(rows, cols) : 0;
+  if (need > 0 && (workspace == nullptr || ws_bytes < need)) return FP8_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return FP8_ERR_ALIGN;
+  return cuda_status(branch_bwd_launch(*in, *out, workspace, stream));
+}
+
+fp8_status fp8_checkpoint_quantize(const fp8_recipe* recipe, const fp8_checkpoint* in,
+                                   int64_t rows, int64_t cols, const float* rstd,
+                                   const void* gamma, int32_t gamma_fp32, int32_t want_row,
+                                   int32_t want_col, fp8_tensor* out, void* workspace,
+                                   size_t ws_bytes, int32_t* dev_status, cudaStream_t stream) {
+  (void)dev_status;                         // no device-side waits in this path
+  if (in == nullptr) return FP8_ERR_NULL;
+  if (!want_row && !want_col) return FP8_ERR_SHAPE;
+  NormArgs a{};
+  a.gamma = gamma;
+  a.gamma_fp32 = gamma_fp32;
+  a.rows = rows;
+  a.cols = cols;
+  a.rstd = const_cast<float*>(rstd);        // read only
+  FP8_TRY(check_norm(recipe, want_row, want_col, out, &a, workspace, ws_bytes, false));
+  if ((rstd == nullptr) != (gamma == nullptr)) return FP8_ERR_NULL;
+  const bool empty = rows == 0 || cols == 0;
+  if (!empty) {
+    FP8_TRY(check_checkpoint(in));
+    FP8_TRY(check_vector(gamma, gamma_fp32));
+  }
+  set_norm_out(a, out);
+  if (empty) return empty_norm(a, want_row, want_col, out, workspace, stream);
+  return cuda_status(checkpoint_quantize_launch(a, *in, out, workspace, stream));
 }
 
 }  // extern "C"

@@ -1,7 +1,8 @@
 // Activation checkpoints in 8 bits (ckpt.cuh has the format): written from bf16
-// (fp8_checkpoint_write) and read back (fp8_checkpoint_read).
+// (fp8_checkpoint_write), read back (fp8_checkpoint_read), and made into the FP8 copies that the
+// linear layer reads, with the norm in front of it or without (fp8_checkpoint_quantize).
 //
-// Both are one pass over memory, 3 + 1/32 bytes an element. A thread has 16 columns (32 bytes of
+// The first two are one pass over memory, 3 + 1/32 bytes an element. A thread has 16 columns (32 bytes of
 // bf16, 16 of codes); two lanes share a block's scale, eight a word of scales, so a row counts as a
 // whole number of 128 columns and the lanes beyond its end idle.
 #include <algorithm>
@@ -111,7 +112,108 @@ __global__ void __launch_bounds__(kCkptThreads)
   }
 }
 
+// The row copy of y = (h rstd) gamma (or of h) with h from its checkpoint, or, for per-tensor scales,
+// the partials of y's amax; padding rows are zeros. The column copy is the norm's column kernel's.
+// The threads of a CTA lie as in the kernels above; the CTAs stay and walk the units.
+template <int OUT>
+__global__ void __launch_bounds__(kCkptThreads)
+    checkpoint_row_kernel(const __grid_constant__ NormParams p) {
+  __shared__ uint32_t red[kCkptThreads / 32];
+  pdl_wait();
+  const uint32_t row_units = (p.cols + 127) / 128 * 8;
+  // less than 2^30, and a multiple of 32 (padded rows come by 16): whole warps
+  const uint32_t units = uint32_t(p.rows_pad) * row_units, step = gridDim.x * kCkptThreads;
+  const float tensor_scale = OUT == N_TENSOR ? *p.scale_in : 1.0f;
+  uint32_t amax = 0;
+  for (uint32_t at = blockIdx.x * kCkptThreads + threadIdx.x; at < units; at += step) {
+    const int64_t r = at / row_units;
+    const int unit = int(at % row_units), c = 16 * unit;
+    const bool in = c < p.cols, live = in && r < p.rows;
+    float2 y[2][4];
+    if (live) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.ck + r * p.cols + c));
+      const float e = ckpt_factor(__ldg(p.ck_scale + r * ckpt_pitch(p.cols) + (unit >> 1)));
+      const float f = p.rstd == nullptr ? e : e * p.rstd[r];
+      const float2 f2 = make_float2(f, f);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ckpt_widen8(k == 0 ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w), y[k]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[k][i] = __fmul2_rn(y[k][i], f2);
+        if (p.gamma != nullptr) {
+          float2 g[4];
+          gamma_pairs(p.gamma, p.gamma_fp32, p.cols, c + 8 * k, g);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[k][i] = __fmul2_rn(y[k][i], g[i]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[k][i] = make_float2(0.0f, 0.0f);
+    }
+    uint32_t m = max(__float_as_uint(max8_abs(y[0])), __float_as_uint(max8_abs(y[1])));
+    if constexpr (OUT == N_STATS || OUT == N_TENSOR) amax = max(amax, m);
+    if constexpr (OUT != N_STATS) {
+      float s = tensor_scale;
+      if constexpr (OUT == N_MX) {
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        uint32_t w = mx_scale_byte_f32(m, &s) << (4 * (threadIdx.x & 6));
+        w |= __shfl_xor_sync(0xffffffffu, w, 2);
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        if ((unit & 7) == 0)
+          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
+                                       mx_scale_offset32(uint32_t(r), unit >> 1, p.cols)) = w;
+      }
+      if constexpr (OUT == N_BW) {
+#pragma unroll
+        for (int o = 1; o < 8; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float sinv;
+        s = scale_from_amax(__uint_as_float(m), p.margin, &sinv, 448.0f, p.pow2);
+        if ((unit & 7) == 0) {
+          if (p.pow2)
+            *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
+                                         mx_scale_offset32(uint32_t(r), unit >> 1, p.cols)) =
+                e8m0_of_pow2(sinv) * 0x01010101u;
+          else
+            reinterpret_cast<float*>(p.row_scale)[int64_t(unit >> 3) * p.rows_pad + r] = sinv;
+        }
+      }
+      if (in) {
+        const float2 s2 = make_float2(s, s);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 a = __fmul2_rn(y[k >> 1][2 * (k & 1)], s2);
+          const float2 b = __fmul2_rn(y[k >> 1][2 * (k & 1) + 1], s2);
+          w[k] = cvt_e4m3x4(a.x, a.y, b.x, b.y);
+        }
+        *reinterpret_cast<uint4*>(p.row + r * p.cols + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+  if constexpr (OUT == N_STATS || OUT == N_TENSOR) {
+    const uint32_t m = cta_max(amax, red);
+    if (threadIdx.x == 0) p.part[blockIdx.x] = m;
+  }
+  pdl_launch_dependents();
+}
+
 namespace {
+
+cudaError_t checkpoint_rows(int out_kind, const NormParams& p, const void*, int* ctas,
+                            cudaStream_t st) {
+  const int64_t units = p.rows_pad * ((p.cols + 127) / 128 * 8);
+  const unsigned grid = unsigned(std::min<int64_t>((units + kCkptThreads - 1) / kCkptThreads,
+                                                   int64_t(num_sms()) * 8));
+  if (ctas != nullptr) *ctas = int(grid);
+  auto kern = out_kind == N_MX       ? checkpoint_row_kernel<N_MX>
+              : out_kind == N_BW     ? checkpoint_row_kernel<N_BW>
+              : out_kind == N_TENSOR ? checkpoint_row_kernel<N_TENSOR>
+                                     : checkpoint_row_kernel<N_STATS>;
+  return launch_kernel(kern, dim3(grid), dim3(kCkptThreads), 0, st, nullptr, p);
+}
 
 CkptParams ckpt_params(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols,
                        const fp8_checkpoint& c, unsigned* grid) {
@@ -143,6 +245,14 @@ cudaError_t checkpoint_read_launch(const fp8_checkpoint& in, int64_t rows, int64
   unsigned grid;
   const CkptParams p = ckpt_params(x, cols, rows, cols, in, &grid);
   return launch_kernel(checkpoint_read_kernel, dim3(grid), dim3(kCkptThreads), 0, st, nullptr, p);
+}
+
+cudaError_t checkpoint_quantize_launch(const NormArgs& a, const fp8_checkpoint& in,
+                                       fp8_tensor* out, void* workspace, cudaStream_t st) {
+  NormParams p = norm_params(a);
+  p.ck = in.codes;
+  p.ck_scale = in.scale;
+  return norm_copies_launch(a, p, out, workspace, st, checkpoint_rows, nullptr);
 }
 
 }  // namespace fp8lin

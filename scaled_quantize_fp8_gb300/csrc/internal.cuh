@@ -146,8 +146,9 @@ int64_t norm_pad_rows(int kind, int64_t rows);
 cudaError_t norm_quantize_launch(const NormArgs& a, fp8_tensor* out, void* workspace,
                                  cudaStream_t st);
 size_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols);
-cudaError_t norm_bwd_launch(const fp8_norm_grad& a, uint16_t* dh, float* dgamma, void* workspace,
-                            cudaStream_t st);
+// h_ckpt: h's checkpoint instead of a.h, or null.
+cudaError_t norm_bwd_launch(const fp8_norm_grad& a, const fp8_checkpoint* h_ckpt, uint16_t* dh,
+                            float* dgamma, void* workspace, cudaStream_t st);
 
 // ---- branch.cu (a block's output joins the stream; the norm in front of the next)
 // a: x is the block's output, res the stream.
@@ -155,11 +156,19 @@ cudaError_t branch_quantize_launch(const NormArgs& a, const fp8_branch_input& in
                                    const fp8_checkpoint* o_ckpt, const fp8_checkpoint* h_ckpt,
                                    fp8_tensor* out, void* workspace, cudaStream_t st);
 
+// ---- branch_bwd.cu
+size_t branch_bwd_workspace_bytes(int64_t rows, int64_t cols);
+cudaError_t branch_bwd_launch(const fp8_branch_grad& a, const fp8_branch_grad_out& out,
+                              void* workspace, cudaStream_t st);
+
 // ---- checkpoint.cu (activations in 8 bits)
 cudaError_t checkpoint_write_launch(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols,
                                     const fp8_checkpoint& out, cudaStream_t st);
 cudaError_t checkpoint_read_launch(const fp8_checkpoint& in, int64_t rows, int64_t cols,
                                    uint16_t* x, cudaStream_t st);
+// a: rstd and gamma (both read only, both may be null) and what is wanted; x and h are not looked at.
+cudaError_t checkpoint_quantize_launch(const NormArgs& a, const fp8_checkpoint& in,
+                                       fp8_tensor* out, void* workspace, cudaStream_t st);
 
 // ---- grad.cu (global gradient norm, clipping)
 size_t grad_workspace_bytes(int n);

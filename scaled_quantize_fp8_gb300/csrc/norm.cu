@@ -20,6 +20,7 @@
 // meanwhile. A kernel for the statistics and then one for both copies took 55.8.
 #include <algorithm>
 
+#include "ckpt.cuh"
 #include "common.cuh"
 #include "internal.cuh"
 #include "norm.cuh"
@@ -241,18 +242,28 @@ constexpr int col_ctas() {
   return OUT == N_TENSOR && FULL ? 6 : 5;
 }
 
+template <bool CK>
 struct NormColSmem {
   uint4 slots[2][128][8];
   alignas(16) float rstd[2][128];
   uint32_t red[4];
 };
+// From a checkpoint: 64 bytes a row, eight rows 16 bytes apart from the next eight, so that the rows
+// that 16 lanes read at once lie in different banks; a row's factor for each 32 columns.
+template <>
+struct NormColSmem<true> {
+  uint4 slots[2][128 * 4 + 16];
+  alignas(16) float rstd[2][2][128];
+  uint32_t red[4];
+};
 
 // FULL: nothing but the FP8 column copy is wanted and every tile lies inside the padded tensor,
 // so nothing is tested per row (8192 x 4096, both copies: 48.7 us, else 52.6, with a few spills).
-template <int OUT, bool FULL>
+// CK: h comes from its checkpoint (fp8_checkpoint_quantize).
+template <int OUT, bool FULL, bool CK>
 __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
     norm_col_kernel(const __grid_constant__ NormParams p, const int tiles_c, const int tiles_r) {
-  __shared__ NormColSmem S;
+  __shared__ NormColSmem<CK> S;
   const int t = threadIdx.x, lane = t & 31, w = t >> 5, l2 = lane >> 4, l16 = lane & 15;
   const int c0 = (int(blockIdx.x) % tiles_c) * 64, c = c0 + 16 * w + 8 * l2;
   const int step = int(gridDim.x) / tiles_c;
@@ -267,33 +278,58 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
   const uint64_t first = ptx::l2_evict_first_policy();
   const uint64_t policy = p.res != nullptr ? ptx::l2_evict_normal_policy() : first;
   const auto prefetch = [&](int tile, int buf) {
-    // thread t copies piece t % 8 of the rows t / 8, t / 8 + 16, ..
-    const int64_t r0 = int64_t(tile) * 128, r = r0 + (t >> 3);
-    const int piece = t & 7, cp = c0 + 8 * piece;
-    const uint16_t* x = p.h + r * p.ldx + cp;
-    const bool whole = cp < p.cols && r0 + 128 <= p.rows;
+    if constexpr (CK) {
+      // thread t copies piece t % 4 of the rows t / 4, t / 4 + 32, ..
+      const int64_t r0 = int64_t(tile) * 128;
+      const int piece = t & 3, cp = c0 + 16 * piece;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = (t >> 3) + 16 * i;
-      uint4* d = &S.slots[buf][row][piece ^ ((row >> 3) & 7)];
-      if (whole) {
-        ptx::cp_async_16_hint(d, x, policy);
-      } else {                                                   // nothing read beyond: zeros
-        const uint32_t n = cp < p.cols && r + 16 * i < p.rows ? 16u : 0u;
-        ptx::cp_async_16_zfill_hint(d, n ? x : p.h, n, policy);
+      for (int i = 0; i < 4; ++i) {
+        const int row = (t >> 2) + 32 * i;
+        const uint32_t n = cp < p.cols && r0 + row < p.rows ? 16u : 0u;
+        ptx::cp_async_16_zfill_hint(&S.slots[buf][row * 4 + (row >> 3) + piece],
+                                    n ? p.ck + (r0 + row) * p.cols + cp : p.ck, n, first);
       }
-      x += 16 * p.ldx;
+      ptx::cp_async_commit();
+      if (r0 + t >= p.rows) return make_float2(0.0f, 0.0f);
+      const uint32_t e = *reinterpret_cast<const uint16_t*>(
+          p.ck_scale + (r0 + t) * ckpt_pitch(p.cols) + (c0 >> 5));
+      const float rs = p.rstd == nullptr ? 1.0f : p.rstd[r0 + t];
+      return make_float2(ckpt_factor(e & 0xFFu) * rs, ckpt_factor(e >> 8) * rs);
+    } else {
+      // thread t copies piece t % 8 of the rows t / 8, t / 8 + 16, ..
+      const int64_t r0 = int64_t(tile) * 128, r = r0 + (t >> 3);
+      const int piece = t & 7, cp = c0 + 8 * piece;
+      const uint16_t* x = p.h + r * p.ldx + cp;
+      const bool whole = cp < p.cols && r0 + 128 <= p.rows;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int row = (t >> 3) + 16 * i;
+        uint4* d = &S.slots[buf][row][piece ^ ((row >> 3) & 7)];
+        if (whole) {
+          ptx::cp_async_16_hint(d, x, policy);
+        } else {                                                   // nothing read beyond: zeros
+          const uint32_t n = cp < p.cols && r + 16 * i < p.rows ? 16u : 0u;
+          ptx::cp_async_16_zfill_hint(d, n ? x : p.h, n, policy);
+        }
+        x += 16 * p.ldx;
+      }
+      ptx::cp_async_commit();
+      // padding rows: rstd 0, so that y = (0 0) gamma = 0
+      return r0 + t < p.rows ? p.rstd[r0 + t] : 0.0f;
     }
-    ptx::cp_async_commit();
-    // padding rows: rstd 0, so that y = (0 0) gamma = 0
-    return r0 + t < p.rows ? p.rstd[r0 + t] : 0.0f;
   };
 
   // Last tiles first: the row kernel wrote the last rows of h most recently.
   int tile = tiles_r - 1 - int(blockIdx.x) / tiles_c;
-  float next_rstd = tile >= 0 ? prefetch(tile, 0) : 0.0f;
+  auto next_rstd = decltype(prefetch(0, 0)){};
+  if (tile >= 0) next_rstd = prefetch(tile, 0);
   float2 g[4];
-  gamma_pairs(p.gamma, p.gamma_fp32, p.cols, c, g);
+  if (CK && p.gamma == nullptr) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) g[k] = make_float2(1.0f, 1.0f);
+  } else {
+    gamma_pairs(p.gamma, p.gamma_fp32, p.cols, c, g);
+  }
   float scale = 1.0f;
   if constexpr (OUT == N_TENSOR) {
     uint32_t m = 0;
@@ -315,18 +351,35 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
 
   for (int buf = 0; tile >= 0; tile -= step, buf ^= 1) {
     const int64_t r0 = int64_t(tile) * 128, r = r0 + 8 * l16;
-    S.rstd[buf][t] = next_rstd;
+    if constexpr (CK) {
+      S.rstd[buf][0][t] = next_rstd.x;
+      S.rstd[buf][1][t] = next_rstd.y;
+    } else {
+      S.rstd[buf][t] = next_rstd;
+    }
     ptx::cp_async_wait<0>();
     __syncthreads();                               // the tile is there, the last one read
     if (tile >= step) next_rstd = prefetch(tile - step, buf ^ 1);
     float2 y[8][4];
     {
-      const float4 ra = *reinterpret_cast<const float4*>(&S.rstd[buf][8 * l16]);
-      const float4 rb = *reinterpret_cast<const float4*>(&S.rstd[buf][8 * l16 + 4]);
+      const float* rp;
+      if constexpr (CK) rp = &S.rstd[buf][w >> 1][8 * l16];
+      else rp = &S.rstd[buf][8 * l16];
+      const float4 ra = *reinterpret_cast<const float4*>(rp);
+      const float4 rb = *reinterpret_cast<const float4*>(rp + 4);
       const float rs[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        norm_row8(S.slots[buf][8 * l16 + i][(2 * w + l2) ^ (l16 & 7)], rs[i], g, y[i]);
+      for (int i = 0; i < 8; ++i) {
+        if constexpr (CK) {
+          ckpt_widen8(reinterpret_cast<const uint2*>(
+                          &S.slots[buf][(8 * l16 + i) * 4 + l16 + w])[l2], y[i]);
+          const float2 f = make_float2(rs[i], rs[i]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) y[i][k] = __fmul2_rn(__fmul2_rn(y[i][k], f), g[k]);
+        } else {
+          norm_row8(S.slots[buf][8 * l16 + i][(2 * w + l2) ^ (l16 & 7)], rs[i], g, y[i]);
+        }
+      }
     }
     // padding rows: (0 0) gamma has gamma's sign, theirs is +0 (FULL: at the stores)
     if (!FULL && int(r0) + 128 > int(p.rows)) {
@@ -439,7 +492,7 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
       // by way of the tile's buffer (64 bytes a row, 8-byte units exchanged like the pieces), so
       // that four lanes write 64 consecutive bytes
       __syncthreads();
-      uint2* codes = reinterpret_cast<uint2*>(&S.slots[buf][0][0]);
+      uint2* codes = reinterpret_cast<uint2*>(&S.slots[buf]);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         codes[(8 * l16 + i) * 8 + ((2 * w + l2) ^ (l16 & 7))] =
@@ -547,18 +600,22 @@ cudaError_t norm_rows(int out_kind, const NormParams& p, const void*, int* ctas,
                                 : launch_rows<N_STATS>(p, ctas, st);
 }
 
-template <int OUT>
+template <int OUT, bool CK>
 cudaError_t launch_cols(const NormParams& p, cudaStream_t st) {
   const int tiles_c = (p.cols + 63) / 64;
   const int tiles_r = int((p.rows_pad + 127) / 128);
   const bool full = (OUT != N_TENSOR || p.row == nullptr) && p.col != nullptr && !p.col_bf16 &&
                     p.cols % 64 == 0 && p.rows_pad % 128 == 0;
-  auto kern = full ? norm_col_kernel<OUT, true> : norm_col_kernel<OUT, false>;
+  auto kern = full ? norm_col_kernel<OUT, true, CK> : norm_col_kernel<OUT, false, CK>;
   // every CTA keeps its column block (and gamma): a whole number of CTAs per block
   const int ctas = full ? col_ctas<OUT, true>() : col_ctas<OUT, false>();
   const int per_block = std::min(tiles_r, std::max(1, num_sms() * ctas / tiles_c));
   return launch_kernel(kern, dim3(unsigned(per_block * tiles_c)), dim3(128), 0, st, nullptr, p,
                        tiles_c, tiles_r);
+}
+template <int OUT>
+cudaError_t launch_cols(const NormParams& p, cudaStream_t st) {
+  return p.ck != nullptr ? launch_cols<OUT, true>(p, st) : launch_cols<OUT, false>(p, st);
 }
 
 }  // namespace
@@ -614,16 +671,18 @@ cudaError_t norm_copies_launch(const NormArgs& a, NormParams p, fp8_tensor* out,
 
   // Rows: h, rstd, the row copy where its scale is known by then.
   const bool cols = a.want_col || tensorwise;
-  if (p.rstd == nullptr && cols) p.rstd = reinterpret_cast<float*>(workspace);
+  if (p.rstd == nullptr && p.ck == nullptr && cols) p.rstd = reinterpret_cast<float*>(workspace);
   p.keep_h = cols;
   if (out_kind == N_TENSOR) {
     p.part = part;
     if (!tensorwise) p.scale_in = out->scale;
   }
   int ctas = 0;
-  const cudaError_t e =
-      rows(p.row == nullptr || tensorwise ? int(N_STATS) : out_kind, p, more, &ctas, st);
-  if (e != cudaSuccess) return e;
+  if (p.ck == nullptr || p.row != nullptr || out_kind == N_TENSOR) {   // (else no statistics)
+    const cudaError_t e =
+        rows(p.row == nullptr || tensorwise ? int(N_STATS) : out_kind, p, more, &ctas, st);
+    if (e != cudaSuccess) return e;
+  }
   if (!cols) {
     if (out_kind != N_TENSOR) return cudaSuccess;
     return launch_kernel(norm_amax_kernel, dim3(1), dim3(512), 0, st, nullptr,

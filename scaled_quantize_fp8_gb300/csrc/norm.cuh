@@ -94,6 +94,8 @@ struct NormParams {
   int pow2;                   // blockwise: power-of-two scales in the MXFP8 layout
   int col_bf16;
   int keep_h;                 // row kernel: h (x without a residual) is read again, from L2
+  const uint8_t* ck;          // the checkpoint of h instead of x and h (ckpt.cuh), or null; then
+  const uint8_t* ck_scale;    // rstd and gamma, read only, may both be null: y is h
 };
 
 // |a|, |b|, |c|: the largest; NaN if one of them is.

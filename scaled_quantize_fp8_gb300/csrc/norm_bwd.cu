@@ -13,6 +13,7 @@
 // next one is on its way while it is worked on.
 #include <algorithm>
 
+#include "ckpt.cuh"
 #include "common.cuh"
 #include "internal.cuh"
 #include "norm.cuh"
@@ -22,7 +23,9 @@ namespace fp8lin {
 
 struct NormBwdParams {
   const uint16_t* dy;
-  const uint16_t* h;
+  const uint16_t* h;          // or its checkpoint:
+  const uint8_t* h_codes;
+  const uint8_t* h_scale;
   const uint16_t* dres;       // or null
   const void* gamma;
   const float* rstd;
@@ -42,11 +45,12 @@ struct NormBwdParams {
 // widened dy and xh stay in registers in between, beyond that they are made again from the
 // slots. Products and sums are fp32, two an instruction (one at a time: 39 instructions an element
 // instead of 21, 55 us at 8192 x 4096).
-template <int V, bool DRES>
+// CK: h comes from its checkpoint, a code's value times its block's power of two and rstd.
+template <int V, bool DRES, bool CK>
 __global__ void __maxnreg__(V <= 2 ? 104 : 128)
     norm_bwd_kernel(const __grid_constant__ NormBwdParams p) {
   constexpr bool kKeep = V <= 2, kGammaRegs = V <= 4;
-  constexpr int kBufs = V <= 4 ? 2 : 1, kIn = DRES ? 3 : 2;
+  constexpr int kBufs = V <= 4 ? 2 : 1, kIn = (CK ? 1 : 2) + DRES, kRes = CK ? 1 : 2;
   __shared__ alignas(16) float red[2][16];
   extern __shared__ uint4 slots[];
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
@@ -54,20 +58,26 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
   if (tid < 32) red[tid >> 4][tid & 15] = 0.0f;     // the unused warps' sums
   if (warps > 1) __syncthreads();
+  // a buffer: dy, h (without a checkpoint), dres as 16-byte pieces, then the checkpoint's 8-byte ones
+  const int pitch = kIn * V * nt + (CK ? V * nt / 2 : 0);
   pdl_wait();
 
   float next_rstd = 0.0f;
+  uint32_t next_e[CK ? V : 1];
   const auto prefetch = [&](int64_t r, int buf) {
     const uint16_t* dy = p.dy + r * p.ld_dy + 8 * lane;
-    const uint16_t* h = p.h + r * p.ld_h + 8 * lane;
+    const uint16_t* h = CK ? nullptr : p.h + r * p.ld_h + 8 * lane;
+    const uint8_t* hc = CK ? p.h_codes + r * p.cols + 8 * lane : nullptr;
     const uint16_t* dr = DRES ? p.dres + r * p.ld_dres + 8 * lane : nullptr;
-    uint4* s = slots + buf * kIn * V * nt + tid;
+    uint4* s = slots + buf * pitch + tid;
+    uint2* c = reinterpret_cast<uint2*>(slots + buf * pitch + kIn * V * nt) + tid;
     if (V * tpr == nv && r < p.rows) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         ptx::cp_async_16(s + j * nt, dy + 8 * j * tpr);
-        ptx::cp_async_16(s + (V + j) * nt, h + 8 * j * tpr);
-        if (DRES) ptx::cp_async_16(s + (2 * V + j) * nt, dr + 8 * j * tpr);
+        if (CK) ptx::cp_async_8(c + j * nt, hc + 8 * j * tpr);
+        else ptx::cp_async_16(s + (V + j) * nt, h + 8 * j * tpr);
+        if (DRES) ptx::cp_async_16(s + (kRes * V + j) * nt, dr + 8 * j * tpr);
       }
     } else {
 #pragma unroll
@@ -75,12 +85,20 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
         const bool in = r < p.rows && j * tpr + lane < nv;
         const uint32_t n = in ? 16u : 0u;
         ptx::cp_async_16_zfill(s + j * nt, in ? dy + 8 * j * tpr : p.dy, n);
-        ptx::cp_async_16_zfill(s + (V + j) * nt, in ? h + 8 * j * tpr : p.h, n);
-        if (DRES) ptx::cp_async_16_zfill(s + (2 * V + j) * nt, in ? dr + 8 * j * tpr : p.dres, n);
+        if (CK) ptx::cp_async_8_zfill(c + j * nt, in ? hc + 8 * j * tpr : p.h_codes, n >> 1);
+        else ptx::cp_async_16_zfill(s + (V + j) * nt, in ? h + 8 * j * tpr : p.h, n);
+        if (DRES)
+          ptx::cp_async_16_zfill(s + (kRes * V + j) * nt, in ? dr + 8 * j * tpr : p.dres, n);
       }
     }
     ptx::cp_async_commit();
     next_rstd = r < p.rows ? p.rstd[r] : 0.0f;
+    if constexpr (CK) {
+      const uint8_t* e = p.h_scale + r * ckpt_pitch(p.cols);
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        next_e[j] = r < p.rows && j * tpr + lane < nv ? __ldg(e + ((j * tpr + lane) >> 2)) : 0u;
+    }
   };
   const int64_t step = int64_t(gridDim.x) * rpc;
   int64_t r = int64_t(blockIdx.x) * rpc + grp;
@@ -101,8 +119,25 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
 
   for (int n = 0; r - grp < p.rows; r += step, ++n) {
     const int buf = kBufs == 2 ? n & 1 : 0;
-    const uint4* s = slots + buf * kIn * V * nt + tid;
+    const uint4* s = slots + buf * pitch + tid;
     const float2 rs = make_float2(next_rstd, next_rstd);
+    float hf[CK ? V : 1];
+    if constexpr (CK) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) hf[j] = ckpt_factor(next_e[j]) * next_rstd;
+    }
+    const auto xh_of = [&](int j, float2 (&x)[4]) {
+      float2 f = rs;
+      if constexpr (CK) {
+        ckpt_widen8((reinterpret_cast<const uint2*>(slots + buf * pitch + kIn * V * nt) +
+                     tid)[j * nt], x);
+        f = make_float2(hf[j], hf[j]);
+      } else {
+        widen8(s[(V + j) * nt], x);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], f);
+    };
     ptx::cp_async_wait<0>();
     if (kBufs == 2 && r + step - grp < p.rows) prefetch(r + step, buf ^ 1);
 
@@ -111,10 +146,9 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
     for (int j = 0; j < V; ++j) {
       float2(&dj)[4] = d[kKeep ? j : 0], (&xj)[4] = x[kKeep ? j : 0], (&gj)[4] = gamma_of(j);
       widen8(s[j * nt], dj);
-      widen8(s[(V + j) * nt], xj);
+      xh_of(j, xj);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        xj[k] = __fmul2_rn(xj[k], rs);
         const float2 t = __fmul2_rn(dj[k], xj[k]);
         acc[j][k] = __fadd2_rn(acc[j][k], t);
         c2 = __ffma2_rn(t, gj[k], c2);
@@ -148,12 +182,10 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
       float2(&dj)[4] = d[kKeep ? j : 0], (&xj)[4] = x[kKeep ? j : 0], (&gj)[4] = gamma_of(j);
       if (!kKeep) {
         widen8(s[j * nt], dj);
-        widen8(s[(V + j) * nt], xj);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) xj[k] = __fmul2_rn(xj[k], rs);
+        xh_of(j, xj);
       }
       float2 e[4];
-      if (DRES) widen8(s[(2 * V + j) * nt], e);
+      if (DRES) widen8(s[(kRes * V + j) * nt], e);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const float2 t = __ffma2_rn(xj[k], cc, __fmul2_rn(dj[k], gj[k]));
@@ -167,7 +199,7 @@ __global__ void __maxnreg__(V <= 2 ? 104 : 128)
     if (kBufs == 1 && r + step - grp < p.rows) prefetch(r + step, 0);
   }
   if (p.part != nullptr) {
-    // the groups' sums, added by the first group in order (slots: 64 V nt bytes or more up to
+    // the groups' sums, added by the first group in order (slots: 48 V nt bytes or more up to
     // four vectors a thread, of which 32 V nt are used here; with eight there is one group)
     float4* sums = reinterpret_cast<float4*>(slots);
     if (rpc > 1) {
@@ -268,14 +300,15 @@ BwdPlan bwd_plan(int64_t rows, int cols) {
   return b;
 }
 
-template <bool DRES>
+template <bool DRES, bool CK>
 cudaError_t launch_bwd(const NormBwdParams& p, const BwdPlan& b, cudaStream_t st) {
   const int v = b.row.v, rpc = b.row.block / b.row.tpr;
-  auto kern = v == 1   ? norm_bwd_kernel<1, DRES>
-              : v == 2 ? norm_bwd_kernel<2, DRES>
-              : v == 4 ? norm_bwd_kernel<4, DRES>
-                       : norm_bwd_kernel<8, DRES>;
-  const size_t smem = size_t(v <= 4 ? 2 : 1) * (DRES ? 3 : 2) * v * b.row.block * 16;
+  auto kern = v == 1   ? norm_bwd_kernel<1, DRES, CK>
+              : v == 2 ? norm_bwd_kernel<2, DRES, CK>
+              : v == 4 ? norm_bwd_kernel<4, DRES, CK>
+                       : norm_bwd_kernel<8, DRES, CK>;
+  const size_t smem =
+      size_t(v <= 4 ? 2 : 1) * (16 + (CK ? 8 : 16) + (DRES ? 16 : 0)) * v * b.row.block;
   if (smem > 47 * 1024) {                                  // 48 KB with the static part
     static ContextOnce attr[4] = {};
     const cudaError_t e = once_per_context(attr[v == 1 ? 0 : v == 2 ? 1 : v == 4 ? 2 : 3], [&] {
@@ -294,8 +327,8 @@ size_t norm_bwd_workspace_bytes(int64_t rows, int64_t cols) {
   return size_t(bwd_plan(rows, int(cols)).grid) * size_t(cols) * 4;
 }
 
-cudaError_t norm_bwd_launch(const fp8_norm_grad& a, uint16_t* dh, float* dgamma, void* workspace,
-                            cudaStream_t st) {
+cudaError_t norm_bwd_launch(const fp8_norm_grad& a, const fp8_checkpoint* h_ckpt, uint16_t* dh,
+                            float* dgamma, void* workspace, cudaStream_t st) {
   const BwdPlan b = bwd_plan(a.rows, int(a.cols));
   NormBwdParams p{};
   p.dy = reinterpret_cast<const uint16_t*>(a.dy);
@@ -314,8 +347,15 @@ cudaError_t norm_bwd_launch(const fp8_norm_grad& a, uint16_t* dh, float* dgamma,
   p.part = dgamma == nullptr ? nullptr
            : b.grid == 1    ? dgamma
                              : reinterpret_cast<float*>(workspace);
-  const cudaError_t e =
-      p.dres != nullptr ? launch_bwd<true>(p, b, st) : launch_bwd<false>(p, b, st);
+  const bool dres = p.dres != nullptr;
+  cudaError_t e;
+  if (h_ckpt != nullptr) {
+    p.h_codes = h_ckpt->codes;
+    p.h_scale = h_ckpt->scale;
+    e = dres ? launch_bwd<true, true>(p, b, st) : launch_bwd<false, true>(p, b, st);
+  } else {
+    e = dres ? launch_bwd<true, false>(p, b, st) : launch_bwd<false, false>(p, b, st);
+  }
   if (e != cudaSuccess || dgamma == nullptr || b.grid == 1) return e;
   return launch_kernel(norm_dgamma_kernel, dim3(unsigned(a.cols / 16)), dim3(256), 0, st, nullptr,
                        static_cast<const float*>(p.part), b.grid, p.cols, dgamma);

@@ -234,6 +234,13 @@ __device__ __forceinline__ void cp_async_8(void* smem_dst, const void* gmem_src)
                "l"(gmem_src)
                : "memory");
 }
+// The same with zeros instead of bytes beyond src_bytes (0 reads nothing).
+__device__ __forceinline__ void cp_async_8_zfill(void* smem_dst, const void* gmem_src,
+                                                 uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(smem_dst)),
+               "l"(gmem_src), "r"(src_bytes)
+               : "memory");
+}
 // 16 bytes global -> shared, bypassing L1; src_bytes < 16 fills the rest with zeros (0 reads
 // nothing, so src may then point anywhere).
 __device__ __forceinline__ void cp_async_16_zfill(void* smem_dst, const void* gmem_src,
@@ -303,6 +310,9 @@ __device__ __forceinline__ void cluster_wait() {
 // Store to another CTA's shared memory (cluster address).
 __device__ __forceinline__ void st_cluster(uint32_t cluster_addr, double v) {
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(cluster_addr), "d"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr), "f"(v) : "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;"
