@@ -516,8 +516,8 @@ typedef struct {
   const void *gate;          /* [cols] or NULL: a gate per channel */
   const float *token_gate;   /* [rows] or NULL: a gate per token (4-byte aligned) */
   const void *gamma;         /* [cols]: weight of the norm in front of the next block */
-  int64_t ld_branch, ld_residual;   /* pitches in elements, multiples of 8, >= cols */
-  int64_t rows, cols;
+  int64_t ld_branch, ld_residual;   /* pitches in elements, multiples of 8, >= cols, <= 2^30 */
+  int64_t rows, cols;               /* rows <= 2^30 */
   int32_t gamma_post_fp32, gate_fp32, gamma_fp32;   /* each: bf16 (0) or fp32 (1) */
   float scale;               /* the residual scale; finite */
   float eps_post, eps;       /* >= 0 and finite, as fp8_norm_input's eps */

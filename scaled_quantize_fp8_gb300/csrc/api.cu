@@ -697,6 +697,8 @@ fp8_status check_checkpoint(const fp8_checkpoint* c) {
   return check_ptr(c->scale);
 }
 
+constexpr int64_t kBranchMaxRows = int64_t(1) << 30;    // and pitch: 32-bit row numbers
+
 constexpr int64_t kCheckpointMaxCols = int64_t(1) << 30;
 
 fp8_status check_checkpoint_shape(int64_t rows, int64_t cols) {
@@ -905,6 +907,8 @@ fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_branc
   FP8_TRY(check_vector(in->gate, in->gate_fp32));
   if (!(in->eps_post >= 0.0f) || !finite(in->eps_post) || !finite(in->scale))
     return FP8_ERR_UNSUPPORTED;
+  if (a.rows > kBranchMaxRows || a.ldx > kBranchMaxRows || a.ldr > kBranchMaxRows)
+    return FP8_ERR_SHAPE;
   const bool empty = a.rows == 0 || a.cols == 0;
   if (!empty) {
     if (a.res == nullptr) return FP8_ERR_NULL;
@@ -954,6 +958,9 @@ fp8_status fp8_branch_rmsnorm_bwd(const fp8_branch_grad* in, const fp8_branch_gr
     }
     return FP8_OK;
   }
+  if (rows > kBranchMaxRows) return FP8_ERR_SHAPE;
+  for (const int64_t ld : {in->ld_dy, in->ld_dres, in->ld_h, in->ld_branch})
+    if (ld > kBranchMaxRows) return FP8_ERR_SHAPE;
   FP8_TRY(check_rows(in->dy, in->ld_dy, cols));
   if (in->dres != nullptr) FP8_TRY(check_rows(in->dres, in->ld_dres, cols));
   const bool h_ckpt = in->h_ckpt.codes != nullptr, branch_ckpt = in->branch_ckpt.codes != nullptr;

@@ -33,69 +33,96 @@ struct BranchParams {
   uint8_t* h_scale;
 };
 
-// Rows on their way: as many as make four vectors a thread, two at least where there is room.
+// Rows on their way while one is worked on.
 template <int V>
 __host__ __device__ constexpr int branch_ahead() {
-  return V == 1 ? 4 : V == 8 ? 1 : 2;
+  return V == 1 ? 4 : V == 2 ? 2 : 1;
+}
+// Shared memory of a thread, for the rows on their way, and of a lane, for w and gamma of its
+// columns. A warp's pieces lie side by side (cp.async of lanes that write 144 bytes apart: 71 us
+// instead of 55).
+template <int V>
+__host__ __device__ constexpr int branch_slot_bytes() {
+  return branch_ahead<V>() * 2 * V * 16;
+}
+__host__ __device__ constexpr int branch_vec_bytes(int v) { return v <= 4 ? v * 64 : 0; }
+
+// tpr threads a row (16, or whole warps); a warp's V vectors a lane follow each other, so that what
+// distinguishes them is a constant in every address: lane l of warp w has the units 32 (V w + j) + l.
+// (With the vectors of a thread tpr units apart, as in the norm's row kernel, 39.7 instructions an
+// element instead of XX.) A row is a chain of two sums, with a barrier each, and every element is
+// worked on about five times, so instructions count as much as bytes: a row's overhead is spread
+// over four vectors a thread, and o, h and y follow each other in the same registers, as floats.
+// The L2 policies as values that may be made again where they are used (no registers kept).
+__device__ __forceinline__ uint64_t policy_first() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ uint64_t policy_last() {
+  uint64_t p;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+  return p;
 }
 
 template <int V, int OUT>
-__global__ void __maxnreg__(V <= 2 ? 80 : 128)
+__global__ void __maxnreg__(V <= 4 ? 80 : 128)
     branch_row_kernel(const __grid_constant__ BranchParams b) {
-  constexpr bool kRegs = V <= 4;        // eight vectors: gamma and w come from L1 every time
+  constexpr bool kSmem = V <= 4;        // eight vectors: gamma and w come from L1 every time
   constexpr int kAhead = branch_ahead<V>();
   const NormParams& p = b.n;
   __shared__ alignas(16) float red[2][16];
   __shared__ uint32_t redm[16];
-  extern __shared__ uint4 slots[];                  // each thread's next rows, then w
+  extern __shared__ uint4 slots[];                  // each thread's next rows, then w and gamma
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
   const int nv = p.cols >> 3, nt = tpr * rpc, tid = grp * tpr + lane;
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
+  const RowUnits at = {V == 1 ? lane : (lane >> 5) * 32 * V + (lane & 31), 32};
+  const bool whole = at.first - (lane & 31) + 32 * V <= nv && warps != 0;   // of the warp
   const bool post = b.gamma_post != nullptr;
   const bool want_y = OUT != N_STATS || p.y != nullptr || p.part != nullptr;
   pdl_wait();
   // As in the norm's row kernel: o, the stream, and the codes go first, h stays until the column
   // kernel has read it.
-  const uint64_t first = ptx::l2_evict_first_policy();
-  const uint64_t hpol = p.keep_h ? ptx::l2_evict_last_policy() : first;
+  const uint64_t first = policy_first();
 
-  const auto prefetch = [&](int64_t r, int buf) {
-    uint4* s = slots + buf * 2 * V * nt + tid;
-    const uint16_t* x = p.x + r * p.ldx + 8 * lane;
-    const uint16_t* res = p.res + r * p.ldr + 8 * lane;
-    if (V * tpr == nv && r < p.rows) {
+  uint4* const slot = slots + (tid >> 5) * (32 * kAhead * 2 * V) + (tid & 31);
+  // (less than 2^31 rows, and as many threads at most beyond them)
+  const uint32_t rows = uint32_t(p.rows), rows_pad = uint32_t(p.rows_pad), cols = p.cols;
+  const uint32_t row_step = gridDim.x * rpc, r_first = blockIdx.x * rpc + grp;
+  const auto prefetch = [&](uint32_t r, int buf) {
+    uint4* s = slot + buf * (32 * 2 * V);
+    const uint16_t* x_next = p.x + uint64_t(r) * uint32_t(p.ldx) + 8 * at.first;
+    const uint16_t* res_next = p.res + uint64_t(r) * uint32_t(p.ldr) + 8 * at.first;
+    if (whole && r < rows) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        ptx::cp_async_16_hint(s + j * nt, x + 8 * j * tpr, first);
-        ptx::cp_async_16_hint(s + (V + j) * nt, res + 8 * j * tpr, first);
+        ptx::cp_async_16_hint(s + 32 * j, x_next + 8 * j * at.step, first);
+        ptx::cp_async_16_hint(s + 32 * (V + j), res_next + 8 * j * at.step, first);
       }
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) {                  // nothing read beyond the tensor: zeros
-        const bool in = r < p.rows && j * tpr + lane < nv;
+        const bool in = r < rows && at(j) < nv;
         const uint32_t n = in ? 16u : 0u;
-        ptx::cp_async_16_zfill_hint(s + j * nt, in ? x + 8 * j * tpr : p.x, n, first);
-        ptx::cp_async_16_zfill_hint(s + (V + j) * nt, in ? res + 8 * j * tpr : p.res, n, first);
+        ptx::cp_async_16_zfill_hint(s + 32 * j, in ? x_next + 8 * j * at.step : p.x, n, first);
+        ptx::cp_async_16_zfill_hint(s + 32 * (V + j), in ? res_next + 8 * j * at.step : p.res, n,
+                                    first);
       }
     }
     ptx::cp_async_commit();
   };
-  const int64_t row_step = int64_t(gridDim.x) * rpc;
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) {
-    const int64_t r0 = int64_t(blockIdx.x) * rpc + k * row_step;
-    if (r0 < p.rows_pad) prefetch(r0 + grp, k);
-    else ptx::cp_async_commit();                    // groups are counted: an empty one
-  }
+  for (int k = 0; k < kAhead; ++k) prefetch(r_first + k * row_step, k);   // (beyond rows: zeros)
   // a token's gate: 0 on padding rows
-  const auto token = [&](int64_t r) {
-    return r >= p.rows ? 0.0f : b.token_gate == nullptr ? 1.0f : __ldg(b.token_gate + r);
+  const auto token = [&](uint32_t r) {
+    return r >= rows ? 0.0f : b.token_gate == nullptr ? 1.0f : __ldg(b.token_gate + r);
   };
 
-  // w of a lane's columns is the same in every row: from shared memory, where there is room, so
-  // that gamma may stay in registers
+  // w and gamma of a lane's columns are the same in every row: as floats from shared memory, where
+  // there is room
   const auto factor = [&](int j, float2 (&w)[4]) {
-    const int c = 8 * (j * tpr + lane);
+    const int c = 8 * at(j);
     float2 g[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = make_float2(1.0f, 1.0f);
@@ -108,103 +135,121 @@ __global__ void __maxnreg__(V <= 2 ? 80 : 128)
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = __fmul2_rn(w[k], make_float2(b.scale, b.scale));
   };
-  float4* ws = reinterpret_cast<float4*>(slots + kAhead * 2 * V * nt) + lane;
-  float2 g[kRegs ? V : 1][4];
-  if (kRegs) {
+  float4* const vec = reinterpret_cast<float4*>(slots + ((nt + 31) >> 5) * (32 * kAhead * 2 * V)) +
+                      (lane >> 5) * (32 * 4 * V) + (lane & 31);
+  if (kSmem) {
     if (grp == 0) {
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         float2 w[4];
         factor(j, w);
-        ws[2 * j * tpr] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
-        ws[(2 * j + 1) * tpr] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
+        vec[32 * 2 * j] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+        vec[32 * (2 * j + 1)] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
+        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * at(j), w);
+        vec[32 * 2 * (V + j)] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+        vec[32 * (2 * (V + j) + 1)] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
       }
-    }
-    if (want_y) {
-#pragma unroll
-      for (int j = 0; j < V; ++j)
-        gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (j * tpr + lane), g[kRegs ? j : 0]);
     }
     __syncthreads();
   }
-  const auto gamma_of = [&](int j) -> float2(&)[4] {
-    if constexpr (!kRegs)
-      gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (j * tpr + lane), g[0]);
-    return g[kRegs ? j : 0];
+  const auto from_smem = [&](int j, float2 (&w)[4]) {
+    const float4 u = vec[32 * 2 * j], v = vec[32 * (2 * j + 1)];
+    w[0] = make_float2(u.x, u.y);
+    w[1] = make_float2(u.z, u.w);
+    w[2] = make_float2(v.x, v.y);
+    w[3] = make_float2(v.z, v.w);
   };
 
   const float tensor_scale = OUT == N_TENSOR ? *p.scale_in : 1.0f;
   uint32_t amax = 0;
   int phase = 0, buf = 0;
-  float next_t = token(int64_t(blockIdx.x) * rpc + grp);
-  for (int64_t r0 = int64_t(blockIdx.x) * rpc; r0 < p.rows_pad; r0 += row_step) {
-    const int64_t r = r0 + grp;
-    const bool live = r < p.rows, stored = r < p.rows_pad;
+  float next_t = token(r_first);
+  for (uint32_t r = r_first; r - grp < rows_pad; r += row_step) {
+    const bool live = r < rows, stored = r < rows_pad;
+    const uint64_t elem = uint64_t(r) * cols + 8 * at.first;     // the thread's first of the row
+    const uint64_t sc = uint64_t(r) * uint32_t(ckpt_pitch(p.cols));
+    const bool full = whole && live;                 // nothing to test per vector
     const float t = next_t;
     next_t = token(r + row_step);
-    uint4 o[V], h[V];
+    float2 x[V][4];                                  // o, then h, then y
     ptx::cp_async_wait<kAhead - 1>();
-    const uint4* s = slots + buf * 2 * V * nt + tid;
+    const uint4* s = slot + buf * (32 * 2 * V);
+    float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int j = 0; j < V; ++j) o[j] = s[j * nt];
+    for (int j = 0; j < V; ++j) {
+      widen8(s[32 * j], x[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q = __ffma2_rn(x[j][k], x[j][k], q);
+    }
     float f = t;
     if (post) {
-      float2 q = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int j = 0; j < V; ++j) add_squares8(o[j], q);
       const float sum = row_sum(q.x + q.y, red, phase, warps, lane, grp, tpr);
       const float ro = rsqrtf(fmaf(sum, p.inv_cols, b.eps_post));
       if (live && lane == 0 && b.rstd_o != nullptr) b.rstd_o[r] = ro;
       f = ro * t;
     }
-    if (b.o_codes != nullptr)
-      ckpt_row<V>(o, b.o_codes + r * p.cols, b.o_scale + r * ckpt_pitch(p.cols), lane, nv, live,
-                  first);
+    if (b.o_codes != nullptr) {
+      if (full)
+        ckpt_row<V, true>(x, b.o_codes + elem, b.o_scale + sc, lane, at, nv, live, first);
+      else
+        ckpt_row<V, false>(x, b.o_codes + elem, b.o_scale + sc, lane, at, nv, live, first);
+    }
 
     // ---- the stream; a gate of 0 leaves it as it is, whatever o holds
     const float2 f2 = make_float2(f, f);
-    uint16_t* ho = p.h + r * p.cols + 8 * lane;
-    const bool all = V * tpr == nv && live;                      // nothing to test per vector
-    float2 q = make_float2(0.0f, 0.0f);
+    q = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      h[j] = s[(V + j) * nt];
+      uint4 h = s[32 * (V + j)];
       if (t != 0.0f) {
-        float2 w[4], x[4], a[4];
-        if (kRegs) {
-          const float4 u = ws[2 * j * tpr], v = ws[(2 * j + 1) * tpr];
-          w[0] = make_float2(u.x, u.y);
-          w[1] = make_float2(u.z, u.w);
-          w[2] = make_float2(v.x, v.y);
-          w[3] = make_float2(v.z, v.w);
-        } else {
-          factor(j, w);
-        }
-        widen8(o[j], x);
-        widen8(h[j], a);
+        float2 w[4], a[4];
+        if (kSmem) from_smem(j, w);
+        else factor(j, w);
+        widen8(h, a);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) a[k] = __ffma2_rn(__fmul2_rn(x[k], f2), w[k], a[k]);
-        h[j] = make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y),
-                          pack_bf16(a[2].x, a[2].y), pack_bf16(a[3].x, a[3].y));
+        for (int k = 0; k < 4; ++k) a[k] = __ffma2_rn(__fmul2_rn(x[j][k], f2), w[k], a[k]);
+        h = make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y),
+                       pack_bf16(a[2].x, a[2].y), pack_bf16(a[3].x, a[3].y));
       }
-      if (!all && j * tpr + lane >= nv) h[j] = make_uint4(0, 0, 0, 0);   // (0 inf: no NaN there)
-      if (all || (live && j * tpr + lane < nv)) stg_v4_policy(ho + 8 * j * tpr, h[j], hpol);
-      add_squares8(h[j], q);
+      if (!whole && at(j) >= nv) h = make_uint4(0, 0, 0, 0);     // (0 inf: no NaN there)
+      if (full || (live && at(j) < nv))
+        stg_v4_policy(p.h + elem + 8 * j * at.step, h, p.keep_h ? policy_last() : first);
+      widen8(h, x[j]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q = __ffma2_rn(x[j][k], x[j][k], q);
     }
-    const int64_t next = r0 + kAhead * row_step;
-    if (next < p.rows_pad) prefetch(next + grp, buf);
-    else ptx::cp_async_commit();
+    prefetch(r + kAhead * row_step, buf);
     buf = buf + 1 == kAhead ? 0 : buf + 1;
 
     const float sum = row_sum(q.x + q.y, red, phase, warps, lane, grp, tpr);
     const float rstd = rsqrtf(fmaf(sum, p.inv_cols, p.eps));
     if (live && lane == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
-    if (b.h_codes != nullptr)
-      ckpt_row<V>(h, b.h_codes + r * p.cols, b.h_scale + r * ckpt_pitch(p.cols), lane, nv, live,
-                  first);
+    if (b.h_codes != nullptr) {
+      if (full)
+        ckpt_row<V, true>(x, b.h_codes + elem, b.h_scale + sc, lane, at, nv, live, first);
+      else
+        ckpt_row<V, false>(x, b.h_codes + elem, b.h_scale + sc, lane, at, nv, live, first);
+    }
     if (!want_y) continue;
-    const float rl = live ? rstd : 0.0f;                         // padding rows: (0 0) gamma = 0
-    norm_row_copy<V, OUT>(p, h, rl, gamma_of, r, live, stored, lane, tensor_scale, first, amax);
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float2 g[4];
+      if (kSmem) from_smem(V + j, g);
+      else gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * at(j), g);
+      // padding rows, and lanes without a column (for the amax): (0 0) gamma = 0
+      const float rl = full || (live && at(j) < nv) ? rstd : 0.0f;
+      const float2 r2 = make_float2(rl, rl);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[j][k] = __fmul2_rn(__fmul2_rn(x[j][k], r2), g[k]);
+    }
+    const auto y_of = [&](int j, bool, float2 (&y)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) y[k] = x[j][k];
+    };
+    if (full)
+      norm_row_copy<V, OUT, true>(p, y_of, r, live, stored, lane, at, tensor_scale, first, amax);
+    else
+      norm_row_copy<V, OUT, false>(p, y_of, r, live, stored, lane, at, tensor_scale, first, amax);
   }
   if constexpr (OUT == N_STATS || OUT == N_TENSOR) {
     if (p.part != nullptr) {
@@ -212,6 +257,7 @@ __global__ void __maxnreg__(V <= 2 ? 80 : 128)
       if (threadIdx.x == 0 && threadIdx.y == 0) p.part[blockIdx.x] = m;
     }
   }
+  ptx::cp_async_wait<0>();
   pdl_launch_dependents();
 }
 
@@ -222,27 +268,32 @@ cudaError_t launch_branch(const NormParams& n, const BranchParams& more, int* ct
                           cudaStream_t st) {
   BranchParams b = more;
   b.n = n;
-  const RowPlan pl = row_plan(n.cols, 2, 256);
+  const RowPlan pl = row_plan(n.cols, 4, 384);
   const int rpc = pl.block / pl.tpr;
-  const int per_sm = (pl.v <= 2 ? 768 : 512) / pl.block;
-  const int64_t grid = std::min<int64_t>((n.rows_pad + rpc - 1) / rpc,
-                                         int64_t(num_sms()) * std::max(1, per_sm));
-  if (ctas != nullptr) *ctas = int(grid);
   auto kern = pl.v == 1   ? branch_row_kernel<1, OUT>
               : pl.v == 2 ? branch_row_kernel<2, OUT>
               : pl.v == 4 ? branch_row_kernel<4, OUT>
                           : branch_row_kernel<8, OUT>;
-  const int ahead = pl.v == 1   ? branch_ahead<1>()
-                    : pl.v == 2 ? branch_ahead<2>()
-                    : pl.v == 4 ? branch_ahead<4>()
-                                : branch_ahead<8>();
-  const size_t smem = size_t(pl.v) * 32 * (size_t(ahead) * pl.block + (pl.v <= 4 ? pl.tpr : 0));
+  const int slot = pl.v == 1   ? branch_slot_bytes<1>()
+                   : pl.v == 2 ? branch_slot_bytes<2>()
+                   : pl.v == 4 ? branch_slot_bytes<4>()
+                               : branch_slot_bytes<8>();
+  const int smem = std::max(pl.block, 32) * slot +
+                   std::max(pl.tpr, 32) * branch_vec_bytes(pl.v);
+  // as many CTAs as run at once, by registers (a quarter of an SM has them for six warps at 80 a
+  // thread, four at 128) and by shared memory (an SM has 227 KB, a CTA takes 1 KB more than it asks
+  // for)
+  const int per_sm =
+      std::min((pl.v <= 4 ? 768 : 512) / pl.block, 227 * 1024 / (smem + 1280));
+  const int64_t grid = std::min<int64_t>((n.rows_pad + rpc - 1) / rpc,
+                                         int64_t(num_sms()) * std::max(1, per_sm));
+  if (ctas != nullptr) *ctas = int(grid);
   if (smem > 47 * 1024) {                          // 48 KB with the static part
     static ContextOnce attr[4] = {};
     const cudaError_t e =
         once_per_context(attr[pl.v == 1 ? 0 : pl.v == 2 ? 1 : pl.v == 4 ? 2 : 3], [&] {
           return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      200 * 1024);
+                                      220 * 1024);
         });
     if (e != cudaSuccess) return e;
   }

@@ -11,6 +11,7 @@
 // go to the workspace and branch_sums_kernel adds them in a fixed order. dh goes on in fp32: its
 // rounding to bf16 is the output's alone.
 #include <algorithm>
+#include <type_traits>
 
 #include "ckpt.cuh"
 #include "common.cuh"
@@ -47,97 +48,117 @@ struct BranchBwdParams {
   int parts;
 };
 
-// Buffers for a row: one that is worked on, the others on their way.
-template <int V, bool HCK, bool OCK>
-__host__ __device__ constexpr int bwd_bufs() {
-  return V <= 2 ? 2 : HCK && OCK ? 2 : 1;
+// Units of eight columns that each CTA of a cluster has of a row's, whole blocks of 32 columns (the
+// last one fewer): 1024 at most.
+__host__ __device__ __forceinline__ int bwd_share(int units, int cluster) {
+  return ((units + 3) / 4 + cluster - 1) / cluster * 4;
 }
+
+// Buffers for a row: one that is worked on, one on its way.
+constexpr int kBwdBufs = 2;
 template <int V, bool HCK, bool OCK>
 __host__ __device__ constexpr int bwd_row_bytes() {      // of a thread
   return V * (32 + (HCK ? 8 : 16) + (OCK ? 8 : 16));
 }
 
-// tpr threads per row, V vectors of eight columns a thread (vector j of lane l: columns 8 (j tpr + l)
-// .., in the second CTA of a pair behind those of the first). Every thread copies its own elements
+// tpr threads per row (16, or whole warps), V vectors of eight columns a thread, laid out as in
+// branch_row_kernel. Every thread copies its own elements
 // of the next row to its own slots of shared memory while it works on the present one, and reads
 // them once for each of the row's three steps: mean(a xh); dh and s; do. Only dh stays in
 // registers in between.
-// PAIR: a row of more than 16384 columns, whose two column sums a thread no longer fit in the
-// registers of one CTA, lies in two CTAs of a cluster; each adds the other's part of the row's
-// sums, which arrive in shared memory.
-template <int V, bool HCK, bool OCK, bool PAIR>
+// CL: a row of more than 8192 columns, whose two column sums a thread no longer fit in the registers
+// of one CTA, lies in the two or four CTAs of a cluster, each of which adds the others' parts of the
+// row's sums, which arrive in shared memory.
+template <int V, bool HCK, bool OCK, int CL>
 __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ BranchBwdParams p) {
-  constexpr bool kVec = V <= 2;                     // gamma and w kept, else from L1 each time
-  constexpr int kBufs = bwd_bufs<V, HCK, OCK>();
+  constexpr int kBufs = kBwdBufs;
   __shared__ alignas(16) float red[2][16];
-  __shared__ float other[2];
+  __shared__ float other[2][CL];
   extern __shared__ uint4 slots[];
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
   const int nt = tpr * rpc, tid = grp * tpr + lane;
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
-  const uint32_t rank = PAIR ? ptx::cluster_rank() : 0;
-  const int all_nv = p.cols >> 3, nv0 = PAIR ? (all_nv + 1) >> 1 : all_nv;
-  const int v0 = rank ? nv0 : 0, nv = rank ? all_nv - nv0 : nv0;     // this CTA's vectors
-  const bool post = p.gamma_post != nullptr;
+  const uint32_t rank = CL > 1 ? ptx::cluster_rank() : 0;
+  // this CTA's vectors: from v0 on (the beginning of a block), nv of them
+  const int all_nv = p.cols >> 3, per = CL > 1 ? bwd_share(all_nv, CL) : all_nv;
+  const int v0 = rank * per, nv = min(per, all_nv - v0);
+  const RowUnits at = {V == 1 ? lane : (lane >> 5) * 32 * V + (lane & 31), 32};   // from v0 on
+  const bool whole = at.first - (lane & 31) + 32 * V <= nv && warps != 0;         // of the warp
+  const bool post = p.gamma_post != nullptr, dres = p.dres != nullptr;
   const bool want_s = post || p.dtoken != nullptr;
-  uint4* const vec = slots;                                          // [kBufs][dy, dres, (h, o)][V]
   constexpr int kVecs = V * (2 + !HCK + !OCK), kHalves = V * (HCK + OCK);
-  uint2* const half = reinterpret_cast<uint2*>(vec + kBufs * kVecs * nt);   // [kBufs][(h, o)][V]
+  const int all_warps = (nt + 31) >> 5;
+  // a warp's pieces side by side: [kBufs][dy, dres, (h, o)][V][32], then [kBufs][(h, o)][V][32]
+  uint4* const vec = slots + (tid >> 5) * (32 * kBufs * kVecs) + (tid & 31);
+  uint2* const half = reinterpret_cast<uint2*>(slots + all_warps * (32 * kBufs * kVecs)) +
+                      (tid >> 5) * (32 * kBufs * kHalves) + (tid & 31);
+  const uint32_t rows = uint32_t(p.rows), cols = p.cols, c0 = 8 * (v0 + at.first);
   pdl_wait();
 
   float next_rstd = 0.0f, next_ro = 0.0f, next_t = 0.0f;
   uint32_t next_he[V], next_oe[V];
-  const auto prefetch = [&](int64_t r, int buf) {
-    uint4* s = vec + buf * kVecs * nt + tid;
-    uint2* q = half + buf * kHalves * nt + tid;
-    const bool live = r < p.rows;
+  const auto prefetch = [&](uint32_t r, int buf) {
+    uint4* s = vec + buf * (32 * kVecs);
+    uint2* q = half + buf * (32 * kHalves);
+    const uint16_t* dy = p.dy + (uint64_t(r) * uint32_t(p.ld_dy) + c0);
+    const uint16_t* dr = p.dres + (uint64_t(r) * uint32_t(p.ld_dres) + c0);
+    const uint16_t* h = HCK ? nullptr : p.h + (uint64_t(r) * uint32_t(p.ld_h) + c0);
+    const uint16_t* o = OCK ? nullptr : p.o + (uint64_t(r) * uint32_t(p.ld_o) + c0);
+    const uint64_t e = uint64_t(r) * cols + c0;
+    if (whole && r < rows) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) {                    // nothing read beyond the tensor: zeros
-      const bool in = live && j * tpr + lane < nv;
-      const int c = 8 * (v0 + j * tpr + lane);
-      const uint32_t n = in ? 16u : 0u, m = in ? 8u : 0u;
-      ptx::cp_async_16_zfill(s + j * nt, in ? p.dy + r * p.ld_dy + c : p.dy, n);
-      if (p.dres != nullptr)
-        ptx::cp_async_16_zfill(s + (V + j) * nt, in ? p.dres + r * p.ld_dres + c : p.dres, n);
-      if (HCK)
-        ptx::cp_async_8_zfill(q + j * nt, in ? p.h_codes + r * p.cols + c : p.h_codes, m);
-      else
-        ptx::cp_async_16_zfill(s + (2 * V + j) * nt, in ? p.h + r * p.ld_h + c : p.h, n);
-      if (OCK)
-        ptx::cp_async_8_zfill(q + ((HCK ? V : 0) + j) * nt,
-                              in ? p.o_codes + r * p.cols + c : p.o_codes, m);
-      else
-        ptx::cp_async_16_zfill(s + ((HCK ? 2 : 3) * V + j) * nt,
-                               in ? p.o + r * p.ld_o + c : p.o, n);
+      for (int j = 0; j < V; ++j) {
+        ptx::cp_async_16(s + 32 * j, dy + 8 * j * at.step);
+        if (dres) ptx::cp_async_16(s + 32 * (V + j), dr + 8 * j * at.step);
+        if (HCK) ptx::cp_async_8(q + 32 * j, p.h_codes + e + 8 * j * at.step);
+        else ptx::cp_async_16(s + 32 * (2 * V + j), h + 8 * j * at.step);
+        if (OCK)
+          ptx::cp_async_8(q + 32 * ((HCK ? V : 0) + j), p.o_codes + e + 8 * j * at.step);
+        else
+          ptx::cp_async_16(s + 32 * ((HCK ? 2 : 3) * V + j), o + 8 * j * at.step);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < V; ++j) {                  // nothing read beyond the tensor: zeros
+        const bool in = r < rows && at(j) < nv;
+        const uint32_t n = in ? 16u : 0u, m = in ? 8u : 0u, d = 8 * j * at.step;
+        ptx::cp_async_16_zfill(s + 32 * j, in ? dy + d : p.dy, n);
+        if (dres) ptx::cp_async_16_zfill(s + 32 * (V + j), in ? dr + d : p.dres, n);
+        if (HCK) ptx::cp_async_8_zfill(q + 32 * j, in ? p.h_codes + e + d : p.h_codes, m);
+        else ptx::cp_async_16_zfill(s + 32 * (2 * V + j), in ? h + d : p.h, n);
+        if (OCK)
+          ptx::cp_async_8_zfill(q + 32 * ((HCK ? V : 0) + j), in ? p.o_codes + e + d : p.o_codes,
+                                m);
+        else
+          ptx::cp_async_16_zfill(s + 32 * ((HCK ? 2 : 3) * V + j), in ? o + d : p.o, n);
+      }
     }
     ptx::cp_async_commit();
   };
   // the row's own numbers, read a row ahead
-  const auto scalars = [&](int64_t r) {
-    const bool live = r < p.rows;
+  const auto scalars = [&](auto full_tag, uint32_t r) {
+    constexpr bool FULL = decltype(full_tag)::value;
+    const bool live = r < rows;
     next_rstd = live ? p.rstd[r] : 0.0f;
     next_ro = !live ? 0.0f : post ? p.rstd_o[r] : 1.0f;
     next_t = !live ? 0.0f : p.token_gate != nullptr ? p.token_gate[r] : 1.0f;
-    const int64_t at = r * ckpt_pitch(p.cols);
+    const uint64_t e = uint64_t(r) * uint32_t(ckpt_pitch(p.cols)) + ((v0 + at.first) >> 2);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const bool in = live && j * tpr + lane < nv;
-      const int b = (v0 + j * tpr + lane) >> 2;
-      if (HCK) next_he[j] = in ? __ldg(p.h_scale + at + b) : 0u;
-      if (OCK) next_oe[j] = in ? __ldg(p.o_scale + at + b) : 0u;
+      const bool in = live && (FULL || at(j) < nv);
+      const uint32_t b = j * at.step / 4;
+      if (HCK) next_he[j] = in ? __ldg(p.h_scale + e + b) : 0u;
+      if (OCK) next_oe[j] = in ? __ldg(p.o_scale + e + b) : 0u;
     }
   };
-  const int64_t step = int64_t(PAIR ? gridDim.x >> 1 : gridDim.x) * rpc;
-  int64_t r = int64_t(PAIR ? blockIdx.x >> 1 : blockIdx.x) * rpc + grp;
+  const uint32_t step = gridDim.x / CL * rpc;
+  uint32_t r = blockIdx.x / CL * rpc + grp;
 #pragma unroll
-  for (int k = 0; k < (kBufs > 1 ? kBufs - 1 : 1); ++k) {
-    if (r - grp + k * step < p.rows) prefetch(r + k * step, k);
-    else ptx::cp_async_commit();                    // groups are counted: an empty one
-  }
-  scalars(r);
+  for (int k = 0; k < kBufs - 1; ++k) prefetch(r + k * step, k);
+  scalars(std::false_type{}, r);
 
   const auto factor = [&](int j, float2 (&w)[4]) {
-    const int c = 8 * (v0 + j * tpr + lane);
+    const int c = 8 * (v0 + at(j));
     float2 g[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = make_float2(1.0f, 1.0f);
@@ -150,61 +171,56 @@ __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ Branc
 #pragma unroll
     for (int k = 0; k < 4; ++k) w[k] = __fmul2_rn(w[k], make_float2(p.scale, p.scale));
   };
-  float4* ws = reinterpret_cast<float4*>(half + kBufs * kHalves * nt) + lane;
-  float2 g[kVec ? V : 1][4], acc_g[V][4], acc_s[V][4];
+  float4* const ws = reinterpret_cast<float4*>(
+                         slots + all_warps * (32 * kBufs * kVecs + 16 * kBufs * kHalves)) +
+                     (lane >> 5) * (32 * 2 * V) + (lane & 31);
+  float2 g[V][4], acc_g[V][4], acc_s[V][4];
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    if (kVec) {
-      gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (v0 + j * tpr + lane), g[kVec ? j : 0]);
-      if (grp == 0) {
-        float2 w[4];
-        factor(j, w);
-        ws[2 * j * tpr] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
-        ws[(2 * j + 1) * tpr] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
-      }
+    gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (v0 + at(j)), g[j]);
+    if (grp == 0) {
+      float2 w[4];
+      factor(j, w);
+      ws[32 * 2 * j] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+      ws[32 * (2 * j + 1)] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) acc_g[j][k] = acc_s[j][k] = make_float2(0.0f, 0.0f);
   }
   __syncthreads();
-  if (PAIR) ptx::cluster_sync();                    // the other CTA runs: its memory may be written
-  const auto gamma_of = [&](int j) -> float2(&)[4] {
-    if constexpr (!kVec)
-      gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * (v0 + j * tpr + lane), g[0]);
-    return g[kVec ? j : 0];
-  };
+  if (CL > 1) ptx::cluster_sync();                  // the others run: their memory may be written
   const auto w_of = [&](int j, float2 (&w)[4]) {
-    if (kVec) {
-      const float4 a = ws[2 * j * tpr], b = ws[(2 * j + 1) * tpr];
-      w[0] = make_float2(a.x, a.y);
-      w[1] = make_float2(a.z, a.w);
-      w[2] = make_float2(b.x, b.y);
-      w[3] = make_float2(b.z, b.w);
-    } else {
-      factor(j, w);
-    }
+    const float4 a = ws[32 * 2 * j], b = ws[32 * (2 * j + 1)];
+    w[0] = make_float2(a.x, a.y);
+    w[1] = make_float2(a.z, a.w);
+    w[2] = make_float2(b.x, b.y);
+    w[3] = make_float2(b.z, b.w);
   };
   int phase = 0;
-  // (row_sum's phase goes by turns; a pair's second number is read before the next barrier of the
-  // cluster but one, so two places suffice)
+  // A cluster's sum: every CTA's part comes to every CTA, by turns to two places. (What is written
+  // two sums later was read before the barrier in between.)
   int turn = 0;
   const auto sum_of = [&](float v) {
     v = row_sum(v, red, phase, warps, lane, grp, tpr);
-    if constexpr (PAIR) {
-      if (lane == 0) ptx::st_cluster_f32(ptx::map_to_rank(&other[turn], rank ^ 1), v);
+    if constexpr (CL > 1) {
+      if (lane < CL) ptx::st_cluster_f32(ptx::map_to_rank(&other[turn][rank], lane), v);
       __syncwarp();
       ptx::cluster_sync();
-      const float w = other[turn];
-      v = rank ? w + v : v + w;                     // the same order in both
+      v = other[turn][0];
+#pragma unroll
+      for (int i = 1; i < CL; ++i) v += other[turn][i];
       turn ^= 1;
     }
     return v;
   };
 
+  // One row. FULL: the row exists and has columns for all vectors of the warp: nothing is tested.
   int buf = 0;
-  for (; r - grp < p.rows; r += step) {
-    const uint4* s = vec + buf * kVecs * nt + tid;
-    const uint2* q = half + buf * kHalves * nt + tid;
+  const auto one_row = [&](auto full_tag) {
+    constexpr bool FULL = decltype(full_tag)::value;
+    const uint4* s = vec + buf * (32 * kVecs);
+    const uint2* q = half + buf * (32 * kHalves);
+    const uint64_t elem = uint64_t(r) * cols + c0;
     const float rs = next_rstd, ro = next_ro, t = next_t;
     float hf[HCK ? V : 1], of[OCK ? V : 1];         // what a code of the row counts in xh and xo
 #pragma unroll
@@ -214,113 +230,116 @@ __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ Branc
     }
     if (!HCK) hf[0] = rs;
     if (!OCK) of[0] = ro;
-    const auto xh_of = [&](int j, float2 (&x)[4]) {
-      if constexpr (HCK) ckpt_widen8(q[j * nt], x);
-      else widen8(s[(2 * V + j) * nt], x);
-      const float2 f = make_float2(hf[HCK ? j : 0], hf[HCK ? j : 0]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], f);
+    // what h and o hold, without those factors: they are applied to sums and to other factors
+    const auto h_of = [&](int j, float2 (&x)[4]) {
+      if constexpr (HCK) ckpt_widen8(q[32 * j], x);
+      else widen8(s[32 * (2 * V + j)], x);
     };
-    const auto xo_of = [&](int j, float2 (&x)[4]) {
-      if constexpr (OCK) ckpt_widen8(q[((HCK ? V : 0) + j) * nt], x);
-      else widen8(s[((HCK ? 2 : 3) * V + j) * nt], x);
-      const float2 f = make_float2(of[OCK ? j : 0], of[OCK ? j : 0]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = __fmul2_rn(x[k], f);
+    const auto o_of = [&](int j, float2 (&x)[4]) {
+      if constexpr (OCK) ckpt_widen8(q[32 * ((HCK ? V : 0) + j)], x);
+      else widen8(s[32 * ((HCK ? 2 : 3) * V + j)], x);
     };
-    if (kBufs > 1) {
-      ptx::cp_async_wait<kBufs - 2>();
-      const int64_t ahead = r + (kBufs - 1) * step;
-      if (ahead - grp < p.rows) prefetch(ahead, buf + kBufs - 1 >= kBufs ? buf - 1 : buf + kBufs - 1);
-      else ptx::cp_async_commit();
-    } else {
-      ptx::cp_async_wait<0>();
-    }
-    scalars(r + step);
+    ptx::cp_async_wait<kBufs - 2>();
+    prefetch(r + (kBufs - 1) * step, buf == 0 ? kBufs - 1 : buf - 1);
+    scalars(full_tag, r + step);
 
     // ---- mean(a xh), dgamma
-    float2 c2 = make_float2(0.0f, 0.0f);
+    float2 d[V][4], x[V][4];                        // dy, then dh, then u; h, then o
+    float c = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float2 d[4], x[4], (&gj)[4] = gamma_of(j);
-      widen8(s[j * nt], d);
-      xh_of(j, x);
+      float2(&xj)[4] = x[j], (&gj)[4] = g[j];
+      widen8(s[32 * j], d[j]);
+      h_of(j, xj);
+      const float f = hf[HCK ? j : 0];
+      const float2 f2 = make_float2(f, f);
+      float2 c2 = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 v = __fmul2_rn(d[k], x[k]);
-        acc_g[j][k] = __fadd2_rn(acc_g[j][k], v);
+        const float2 v = __fmul2_rn(d[j][k], xj[k]);
+        acc_g[j][k] = __ffma2_rn(v, f2, acc_g[j][k]);
         c2 = __ffma2_rn(v, gj[k], c2);
       }
+      c = fmaf(c2.x + c2.y, f, c);
     }
-    const float c = -p.inv_cols * sum_of(c2.x + c2.y);
+    c = -p.inv_cols * sum_of(c);
 
     // ---- dh, s, S
-    const float2 cc = make_float2(c, c), r2 = make_float2(rs, rs), t2 = make_float2(t, t);
-    float2 dh[V][4], s2 = make_float2(0.0f, 0.0f);
+    const float2 r2 = make_float2(rs, rs);
+    float s1 = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float2 d[4], x[4], w[4], (&gj)[4] = gamma_of(j);
-      widen8(s[j * nt], d);
-      xh_of(j, x);
-      if (p.dres != nullptr) {
-        widen8(s[(V + j) * nt], dh[j]);
+      float2 w[4], e[4], (&xj)[4] = x[j], (&gj)[4] = g[j];
+      if (dres) {
+        widen8(s[32 * (V + j)], e);
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dh[j][k] = make_float2(0.0f, 0.0f);
+        for (int k = 0; k < 4; ++k) e[k] = make_float2(0.0f, 0.0f);
       }
+      const float fc = hf[HCK ? j : 0] * c;
+      const float2 fc2 = make_float2(fc, fc);
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        dh[j][k] = __ffma2_rn(r2, __ffma2_rn(x[k], cc, __fmul2_rn(d[k], gj[k])), dh[j][k]);
-      if (r < p.rows && j * tpr + lane < nv)
-        *reinterpret_cast<uint4*>(p.dh + r * p.cols + 8 * (v0 + j * tpr + lane)) = make_uint4(
-            pack_bf16(dh[j][0].x, dh[j][0].y), pack_bf16(dh[j][1].x, dh[j][1].y),
-            pack_bf16(dh[j][2].x, dh[j][2].y), pack_bf16(dh[j][3].x, dh[j][3].y));
-      xo_of(j, x);
+        d[j][k] = __ffma2_rn(r2, __ffma2_rn(xj[k], fc2, __fmul2_rn(d[j][k], gj[k])), e[k]);
+      if (FULL || (r < rows && at(j) < nv))
+        *reinterpret_cast<uint4*>(p.dh + elem + 8 * j * at.step) = make_uint4(
+            pack_bf16(d[j][0].x, d[j][0].y), pack_bf16(d[j][1].x, d[j][1].y),
+            pack_bf16(d[j][2].x, d[j][2].y), pack_bf16(d[j][3].x, d[j][3].y));
+      o_of(j, xj);
       w_of(j, w);
+      const float f = of[OCK ? j : 0], ft = f * t;
+      const float2 ft2 = make_float2(ft, ft);
+      float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const float2 v = __fmul2_rn(dh[j][k], x[k]);
+        const float2 v = __fmul2_rn(d[j][k], xj[k]);
         // a gate of 0: whatever o holds, nothing of it reaches the sums
-        if (t != 0.0f) acc_s[j][k] = __ffma2_rn(t2, v, acc_s[j][k]);
+        if (t != 0.0f) acc_s[j][k] = __ffma2_rn(v, ft2, acc_s[j][k]);
         s2 = __ffma2_rn(v, w[k], s2);
-        dh[j][k] = __fmul2_rn(dh[j][k], w[k]);      // u from here on
+        d[j][k] = __fmul2_rn(d[j][k], w[k]);        // u from here on
       }
+      s1 = fmaf(s2.x + s2.y, f, s1);
     }
     float sum = 0.0f;
     if (want_s) {
-      sum = sum_of(s2.x + s2.y);
-      if (p.dtoken != nullptr && lane == 0 && r < p.rows && rank == 0) p.dtoken[r] = sum;
+      sum = sum_of(s1);
+      if (p.dtoken != nullptr && lane == 0 && (FULL || r < rows) && rank == 0) p.dtoken[r] = sum;
     }
 
     // ---- do
     const float rt = ro * t, m = post ? -p.inv_cols * rt * sum : 0.0f;
-    const float2 rt2 = make_float2(rt, rt), m2 = make_float2(m, m);
+    const float2 rt2 = make_float2(rt, rt);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       if (t == 0.0f) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dh[j][k] = make_float2(0.0f, 0.0f);
+        for (int k = 0; k < 4; ++k) d[j][k] = make_float2(0.0f, 0.0f);
       } else if (post) {
-        float2 x[4];
-        xo_of(j, x);
+        float2(&xj)[4] = x[j];
+        const float fm = of[OCK ? j : 0] * m;
+        const float2 fm2 = make_float2(fm, fm);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dh[j][k] = __ffma2_rn(x[k], m2, __fmul2_rn(dh[j][k], rt2));
+        for (int k = 0; k < 4; ++k)
+          d[j][k] = __ffma2_rn(xj[k], fm2, __fmul2_rn(d[j][k], rt2));
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dh[j][k] = __fmul2_rn(dh[j][k], rt2);
+        for (int k = 0; k < 4; ++k) d[j][k] = __fmul2_rn(d[j][k], rt2);
       }
-      if (r < p.rows && j * tpr + lane < nv)
-        *reinterpret_cast<uint4*>(p.d_o + r * p.cols + 8 * (v0 + j * tpr + lane)) = make_uint4(
-            pack_bf16(dh[j][0].x, dh[j][0].y), pack_bf16(dh[j][1].x, dh[j][1].y),
-            pack_bf16(dh[j][2].x, dh[j][2].y), pack_bf16(dh[j][3].x, dh[j][3].y));
+      if (FULL || (r < rows && at(j) < nv))
+        *reinterpret_cast<uint4*>(p.d_o + elem + 8 * j * at.step) = make_uint4(
+            pack_bf16(d[j][0].x, d[j][0].y), pack_bf16(d[j][1].x, d[j][1].y),
+            pack_bf16(d[j][2].x, d[j][2].y), pack_bf16(d[j][3].x, d[j][3].y));
     }
-    if (kBufs == 1) {
-      if (r + step - grp < p.rows) prefetch(r + step, 0);
-    } else {
-      buf = buf + 1 == kBufs ? 0 : buf + 1;
-    }
+    buf = buf + 1 == kBufs ? 0 : buf + 1;
+  };
+  // All warps of a group make the same rows, the existing ones, for they meet at its barriers; the
+  // two groups of a warp go on together.
+  if (whole) {
+    for (; r < rows; r += step) one_row(std::true_type{});
+  } else {
+    for (; warps != 0 ? r < rows : r - grp < rows; r += step) one_row(std::false_type{});
   }
-
+  ptx::cp_async_wait<0>();
   if (p.part != nullptr) {
     // the groups' sums, added by the first group in order, by way of the slots (96 V nt bytes or
     // more where there are several groups, of which 64 V nt are used)
@@ -356,16 +375,16 @@ __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ Branc
           }
         }
       }
-      const int64_t at = int64_t(PAIR ? blockIdx.x >> 1 : blockIdx.x) * p.cols;
-      float* dst = p.part + at + 8 * (v0 + lane);
+      const int64_t part = int64_t(blockIdx.x / CL) * p.cols;
+      float* dst = p.part + part + c0;
       const int64_t to_s = int64_t(p.parts) * p.cols;
 #pragma unroll
       for (int j = 0; j < V; ++j) {
-        if (j * tpr + lane < nv) {
-          float4* q = reinterpret_cast<float4*>(dst + 8 * j * tpr);
+        if (at(j) < nv) {
+          float4* q = reinterpret_cast<float4*>(dst + 8 * j * at.step);
           q[0] = make_float4(acc_g[j][0].x, acc_g[j][0].y, acc_g[j][1].x, acc_g[j][1].y);
           q[1] = make_float4(acc_g[j][2].x, acc_g[j][2].y, acc_g[j][3].x, acc_g[j][3].y);
-          q = reinterpret_cast<float4*>(dst + to_s + 8 * j * tpr);
+          q = reinterpret_cast<float4*>(dst + to_s + 8 * j * at.step);
           q[0] = make_float4(acc_s[j][0].x, acc_s[j][0].y, acc_s[j][1].x, acc_s[j][1].y);
           q[1] = make_float4(acc_s[j][2].x, acc_s[j][2].y, acc_s[j][3].x, acc_s[j][3].y);
         }
@@ -442,31 +461,31 @@ __global__ void __launch_bounds__(256)
 namespace {
 
 struct BranchBwdPlan {
-  RowPlan row;
-  bool pair;
-  int parts;                  // CTAs, or pairs of them
+  RowPlan row;                // of a CTA's part of a row
+  int cluster;                // CTAs that share a row
+  int parts;                  // CTAs, or clusters of them
 };
 // One CTA of up to 512 threads per SM, as in the norm's backward pass: its row groups' column sums
 // meet in shared memory, so there are at most as many partials as SMs. Few rows: one vector a
 // thread, and fewer rows a CTA while there are SMs without any.
 BranchBwdPlan branch_bwd_plan(int64_t rows, int64_t cols) {
   BranchBwdPlan b;
-  const int sms = num_sms();
-  b.pair = cols > 16384;
-  const int mine = b.pair ? int(cols / 8 + 1) / 2 * 8 : int(cols);
-  b.row = row_plan(mine, rows <= 4 * sms ? 1 : 2, 512);
+  const int sms = num_sms(), nv = int(cols / 8);
+  b.cluster = cols > 16384 ? 4 : cols > 8192 ? 2 : 1;
+  const int mine = b.cluster > 1 ? bwd_share(nv, b.cluster) : nv;
+  b.row = row_plan(8 * mine, rows <= 4 * sms ? 1 : 2, 512);
   int rpc = b.row.block / b.row.tpr;
   while (rpc > 1 && (rpc / 2) * b.row.tpr >= 128 && rows <= int64_t(rpc / 2) * sms) rpc /= 2;
   b.row.block = rpc * b.row.tpr;
-  b.parts = int(std::min<int64_t>((rows + rpc - 1) / rpc, b.pair ? sms / 2 : sms));
+  b.parts = int(std::min<int64_t>((rows + rpc - 1) / rpc, sms / b.cluster));
   return b;
 }
 
-template <int V, bool HCK, bool OCK, bool PAIR>
+template <int V, bool HCK, bool OCK, int CL>
 cudaError_t launch_bwd(const BranchBwdParams& p, const BranchBwdPlan& b, cudaStream_t st) {
-  auto kern = branch_bwd_kernel<V, HCK, OCK, PAIR>;
-  const size_t smem = size_t(bwd_bufs<V, HCK, OCK>()) * bwd_row_bytes<V, HCK, OCK>() * b.row.block +
-                      (V <= 2 ? size_t(V) * 32 * b.row.tpr : 0);
+  auto kern = branch_bwd_kernel<V, HCK, OCK, CL>;
+  const size_t smem = size_t(kBwdBufs) * bwd_row_bytes<V, HCK, OCK>() * std::max(b.row.block, 32) +
+                      size_t(V) * 32 * std::max(b.row.tpr, 32);
   if (smem > 47 * 1024) {                                  // 48 KB with the static part
     static ContextOnce attr = {};
     const cudaError_t e = once_per_context(attr, [&] {
@@ -476,19 +495,17 @@ cudaError_t launch_bwd(const BranchBwdParams& p, const BranchBwdPlan& b, cudaStr
   }
   cudaLaunchAttribute cluster = {};
   cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = 2;
+  cluster.val.clusterDim.x = CL;
   cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
   const int rpc = b.row.block / b.row.tpr;
-  return launch_kernel(kern, dim3(unsigned(PAIR ? 2 * b.parts : b.parts)),
-                       dim3(unsigned(b.row.tpr), unsigned(rpc)), smem, st,
-                       PAIR ? &cluster : nullptr, p);
+  return launch_kernel(kern, dim3(unsigned(CL * b.parts)), dim3(unsigned(b.row.tpr), unsigned(rpc)),
+                       smem, st, CL > 1 ? &cluster : nullptr, p);
 }
 template <bool HCK, bool OCK>
 cudaError_t launch_bwd(const BranchBwdParams& p, const BranchBwdPlan& b, cudaStream_t st) {
-  if (b.pair) return launch_bwd<4, HCK, OCK, true>(p, b, st);
-  return b.row.v == 1   ? launch_bwd<1, HCK, OCK, false>(p, b, st)
-         : b.row.v == 2 ? launch_bwd<2, HCK, OCK, false>(p, b, st)
-                        : launch_bwd<4, HCK, OCK, false>(p, b, st);
+  if (b.cluster == 4) return launch_bwd<2, HCK, OCK, 4>(p, b, st);
+  if (b.cluster == 2) return launch_bwd<2, HCK, OCK, 2>(p, b, st);
+  return b.row.v == 1 ? launch_bwd<1, HCK, OCK, 1>(p, b, st) : launch_bwd<2, HCK, OCK, 1>(p, b, st);
 }
 
 }  // namespace

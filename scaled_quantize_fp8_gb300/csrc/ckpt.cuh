@@ -43,23 +43,32 @@ __device__ __forceinline__ void ckpt_widen8(uint2 c, float2 (&f)[4]) {
   }
 }
 
-// The checkpoint of a row that lies in the registers of its threads as norm_row_copy takes it
-// (zeros where a lane has no column).
-template <int V>
-__device__ __forceinline__ void ckpt_row(const uint4 (&x)[V], uint8_t* codes, uint8_t* scale,
-                                         int lane, int nv, bool live, uint64_t policy) {
-  const int tpr = blockDim.x, wl = (int(threadIdx.y) * tpr + lane) & 31;
+// The checkpoint of a row that lies in the registers of its threads as norm_row_copy takes it, as
+// floats (zeros where a lane has no column); codes: of the thread's first vector, scale: of the row.
+template <int V, bool FULL>
+__device__ __forceinline__ void ckpt_row(const float2 (&x)[V][4], uint8_t* codes, uint8_t* scale,
+                                         int lane, const RowUnits at, int nv, bool live,
+                                         uint64_t policy) {
+  const int wl = (int(threadIdx.y) * int(blockDim.x) + int(threadIdx.x)) & 31;
   uint32_t m[V];
   float mult[V];
 #pragma unroll
-  for (int j = 0; j < V; ++j) m[j] = bf16x8_mag(x[j]);
+  for (int j = 0; j < V; ++j) m[j] = __float_as_uint(max8_abs(x[j]));
   int v;
-  const uint32_t word = mx_row_word<V>(m, mult, lane, tpr, &v);
+  const uint32_t word = mx_row_word<V>(m, mult, lane, at, &v);
   if (live && v < nv) *reinterpret_cast<uint32_t*>(scale + (v >> 2)) = word;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const uint2 c = encode8(x[j], mx_mult<V>(mult, j, wl), false);
-    if (live && j * tpr + lane < nv) stg_v2_policy(codes + 8 * (j * tpr + lane), c, policy);
+    const float s = mx_mult<V>(mult, j, wl);
+    const float2 s2 = make_float2(s, s);
+    float2 c[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[k] = __fmul2_rn(x[j][k], s2);
+    if (FULL || (live && at(j) < nv))
+      stg_v2_policy(codes + 8 * j * at.step,
+                    make_uint2(cvt_e4m3x4(c[0].x, c[0].y, c[1].x, c[1].y),
+                               cvt_e4m3x4(c[2].x, c[2].y, c[3].x, c[3].y)),
+                    policy);
   }
 }
 

@@ -198,7 +198,11 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
     if (!want_y) continue;
     const float rl = live ? rstd : 0.0f;                         // padding rows: (0 0) gamma = 0
 
-    norm_row_copy<V, OUT>(p, h, rl, gamma_of, r, live, stored, lane, tensor_scale, codes, amax);
+    const auto y_of = [&](int j, bool in, float2 (&y)[4]) {
+      norm_row8(h[j], in ? rl : 0.0f, gamma_of(j), y);
+    };
+    norm_row_copy<V, OUT, false>(p, y_of, r, live, stored, lane, RowUnits{lane, tpr}, tensor_scale,
+                                 codes, amax);
   }
   if constexpr (OUT == N_STATS || OUT == N_TENSOR) {
     if (p.part != nullptr) {

@@ -190,13 +190,20 @@ __device__ __forceinline__ void scatter_max(uint32_t (&m)[V]) {
   }
 }
 
+// Where a thread's vectors lie in its row: vector j holds the eight columns of unit first + j step.
+// The 16 lanes (by their number in the warp, modulo 16) that share a vector have consecutive units.
+struct RowUnits {
+  int first, step;
+  __device__ __forceinline__ int operator()(int j) const { return first + j * step; }
+};
+
 // A row's blocks of 32 columns (four lanes to a vector's block): reduces the lanes' magnitudes m (31
 // bits) and leaves the multipliers of the blocks that this lane scales in mult (see mx_mult). Four
 // blocks, the 16 lanes' share of a vector, make one word of E8M0 bytes: returns a word and in *v
-// the first 8-column unit of its blocks, or a unit beyond every row where another lane has the word.
+// the first unit of its blocks, or a unit beyond every row where another lane has the word.
 template <int V>
 __device__ __forceinline__ uint32_t mx_row_word(uint32_t (&m)[V], float (&mult)[V], int lane,
-                                                int tpr, int* v) {
+                                                const RowUnits at, int* v) {
   constexpr int T = V >= 4 ? V / 4 : 1;                      // blocks that a lane scales
   scatter_max<V, 2>(m);
   const int q = lane & 3, s = (lane >> 2) & 3;
@@ -212,7 +219,7 @@ __device__ __forceinline__ uint32_t mx_row_word(uint32_t (&m)[V], float (&mult)[
   for (int t = 1; t < T; ++t) word = s == t ? w[t] : word;
   const int j = V >= 4 ? T * q + s : V == 2 ? q >> 1 : 0;
   const bool mine = V >= 4 ? s < T : s == 0 && (V == 2 ? (q & 1) == 0 : q == 0);
-  *v = mine ? j * tpr + (lane & ~15) : 0x7fffffff;
+  *v = mine ? at(j) - (lane & 15) : 0x7fffffff;
   return word;
 }
 // The multiplier of this lane's block in vector j (wl: the lane in its warp).
@@ -223,17 +230,16 @@ __device__ __forceinline__ float mx_mult(const float (&mult)[V], int j, int wl) 
 }
 
 // What a row kernel writes of a row that lies in the registers of its threads: bf16(y), the row
-// copy's codes and block scales, or its part of the tensor's amax. Vector j of lane l of the row's
-// blockDim.x threads holds columns 8 (j blockDim.x + l) ..; rl is the row's rstd, 0 on padding rows.
-// y is made twice, for the maxima and for the codes.
-template <int V, int OUT, class Gamma>
-__device__ __forceinline__ void norm_row_copy(const NormParams& p, const uint4 (&h)[V],
-                                              const float rl, const Gamma& gamma_of,
-                                              const int64_t r, const bool live, const bool stored,
-                                              const int lane, const float tensor_scale,
+// copy's codes and block scales, or its part of the tensor's amax. y_of(j, in, y) gives the y of
+// vector j, twice: for the maxima and for the codes (in: whether it lies in the row, where that
+// matters). FULL: all vectors of the warp lie in a row that is stored, so nothing is tested.
+template <int V, int OUT, bool FULL, class Y>
+__device__ __forceinline__ void norm_row_copy(const NormParams& p, const Y& y_of, const int64_t r,
+                                              const bool live, const bool stored, const int lane,
+                                              const RowUnits at, const float tensor_scale,
                                               const uint64_t codes, uint32_t& amax) {
-  const int tpr = blockDim.x, nv = p.cols >> 3;
-  const int wl = (int(threadIdx.y) * tpr + lane) & 31;
+  const int nv = p.cols >> 3;
+  const int wl = (int(threadIdx.y) * int(blockDim.x) + int(threadIdx.x)) & 31;
 
   // ---- the blocks' maxima and multipliers
   uint32_t m[V];
@@ -242,13 +248,13 @@ __device__ __forceinline__ void norm_row_copy(const NormParams& p, const uint4 (
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float2 y[4];
-      norm_row8(h[j], rl, gamma_of(j), y);
+      y_of(j, true, y);
       m[j] = __float_as_uint(max8_abs(y));
     }
   }
   if constexpr (OUT == N_MX) {
     int v;
-    const uint32_t word = mx_row_word<V>(m, mult, lane, tpr, &v);
+    const uint32_t word = mx_row_word<V>(m, mult, lane, at, &v);
     if (stored && v < nv)
       *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
                                    mx_scale_offset32(r, v >> 2, p.cols)) = word;
@@ -257,7 +263,7 @@ __device__ __forceinline__ void norm_row_copy(const NormParams& p, const uint4 (
     scatter_max<V, 8>(m);
     float sinv;
     mult[0] = scale_from_amax(__uint_as_float(m[0]), p.margin, &sinv, 448.0f, p.pow2);
-    const int j = (lane & 15) / (16 / V), v = j * tpr + (lane & ~15);
+    const int j = (lane & 15) / (16 / V), v = at(j) - (lane & 15);
     if (stored && v < nv && (lane & 15) % (16 / V) == 0) {
       if (p.pow2)
         *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
@@ -273,16 +279,15 @@ __device__ __forceinline__ void norm_row_copy(const NormParams& p, const uint4 (
   // their codes are +0.
   const uint32_t kept = live ? 0xffffffffu : 0u;
   uint8_t* row =
-      OUT == N_STATS ? nullptr : p.row + (uint32_t(r) * uint32_t(p.cols) + uint32_t(8 * lane));
+      OUT == N_STATS ? nullptr : p.row + (uint32_t(r) * uint32_t(p.cols) + uint32_t(8 * at.first));
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int v = j * tpr + lane;
-    const bool in = v < nv;                 // uniform over the lanes of a block
+    const int v = at(j);
+    const bool in = FULL || v < nv;         // uniform over the lanes of a block
     float2 y[4];
     // (for the amax, no NaN where a row's rstd is infinite and a lane has no column)
-    const float rj = OUT == N_STATS || OUT == N_TENSOR ? (in ? rl : 0.0f) : rl;
-    norm_row8(h[j], rj, gamma_of(j), y);
-    if (p.y != nullptr && live && in)
+    y_of(j, (OUT != N_STATS && OUT != N_TENSOR) || in, y);
+    if (p.y != nullptr && (FULL || (live && in)))
       *reinterpret_cast<uint4*>(p.y + r * p.cols + 8 * v) =
           make_uint4(pack_bf16(y[0].x, y[0].y), pack_bf16(y[1].x, y[1].y),
                      pack_bf16(y[2].x, y[2].y), pack_bf16(y[3].x, y[3].y));
@@ -296,8 +301,13 @@ __device__ __forceinline__ void norm_row_copy(const NormParams& p, const uint4 (
       const float2 s2 = make_float2(s, s);
 #pragma unroll
       for (int k = 0; k < 4; ++k) y[k] = __fmul2_rn(y[k], s2);
-      if (in && stored)
-        stg_v2_policy(row + 8 * j * tpr,
+      if (FULL)
+        stg_v2_policy(row + 8 * j * at.step,
+                      make_uint2(cvt_e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y),
+                                 cvt_e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y)),
+                      codes);
+      else if (in && stored)
+        stg_v2_policy(row + 8 * j * at.step,
                       make_uint2(cvt_e4m3x4(y[0].x, y[0].y, y[1].x, y[1].y) & kept,
                                  cvt_e4m3x4(y[2].x, y[2].y, y[3].x, y[3].y) & kept),
                       codes);
