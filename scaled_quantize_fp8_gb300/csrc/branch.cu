@@ -10,6 +10,7 @@
 // does, and makes both norms of it, the row copy, and the 8-bit checkpoints of o and h that the
 // backward pass reads. The column copy is made by the norm's column kernel from h.
 #include <algorithm>
+#include <type_traits>
 
 #include "ckpt.cuh"
 #include "common.cuh"
@@ -164,11 +165,13 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
   uint32_t amax = 0;
   int phase = 0, buf = 0;
   float next_t = token(r_first);
-  for (uint32_t r = r_first; r - grp < rows_pad; r += row_step) {
-    const bool live = r < rows, stored = r < rows_pad;
+  uint32_t r = r_first;
+  // One row. FULL: the row exists and has columns for all vectors of the warp: nothing is tested.
+  const auto one_row = [&](auto full_tag) {
+    constexpr bool FULL = decltype(full_tag)::value;
+    const bool live = FULL || r < rows, stored = FULL || r < rows_pad;
     const uint64_t elem = uint64_t(r) * cols + 8 * at.first;     // the thread's first of the row
     const uint64_t sc = uint64_t(r) * uint32_t(ckpt_pitch(p.cols));
-    const bool full = whole && live;                 // nothing to test per vector
     const float t = next_t;
     next_t = token(r + row_step);
     float2 x[V][4];                                  // o, then h, then y
@@ -188,12 +191,8 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
       if (live && lane == 0 && b.rstd_o != nullptr) b.rstd_o[r] = ro;
       f = ro * t;
     }
-    if (b.o_codes != nullptr) {
-      if (full)
-        ckpt_row<V, true>(x, b.o_codes + elem, b.o_scale + sc, lane, at, nv, live, first);
-      else
-        ckpt_row<V, false>(x, b.o_codes + elem, b.o_scale + sc, lane, at, nv, live, first);
-    }
+    if (b.o_codes != nullptr)
+      ckpt_row<V, FULL>(x, b.o_codes + elem, b.o_scale + sc, lane, at, nv, live, first);
 
     // ---- the stream; a gate of 0 leaves it as it is, whatever o holds
     const float2 f2 = make_float2(f, f);
@@ -211,8 +210,8 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
         h = make_uint4(pack_bf16(a[0].x, a[0].y), pack_bf16(a[1].x, a[1].y),
                        pack_bf16(a[2].x, a[2].y), pack_bf16(a[3].x, a[3].y));
       }
-      if (!whole && at(j) >= nv) h = make_uint4(0, 0, 0, 0);     // (0 inf: no NaN there)
-      if (full || (live && at(j) < nv))
+      if (!FULL && at(j) >= nv) h = make_uint4(0, 0, 0, 0);     // (0 inf: no NaN there)
+      if (FULL || (live && at(j) < nv))
         stg_v4_policy(p.h + elem + 8 * j * at.step, h, p.keep_h ? policy_last() : first);
       widen8(h, x[j]);
 #pragma unroll
@@ -224,20 +223,16 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
     const float sum = row_sum(q.x + q.y, red, phase, warps, lane, grp, tpr);
     const float rstd = rsqrtf(fmaf(sum, p.inv_cols, p.eps));
     if (live && lane == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
-    if (b.h_codes != nullptr) {
-      if (full)
-        ckpt_row<V, true>(x, b.h_codes + elem, b.h_scale + sc, lane, at, nv, live, first);
-      else
-        ckpt_row<V, false>(x, b.h_codes + elem, b.h_scale + sc, lane, at, nv, live, first);
-    }
-    if (!want_y) continue;
+    if (b.h_codes != nullptr)
+      ckpt_row<V, FULL>(x, b.h_codes + elem, b.h_scale + sc, lane, at, nv, live, first);
+    if (!want_y) return;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float2 g[4];
       if (kSmem) from_smem(V + j, g);
       else gamma_pairs(p.gamma, p.gamma_fp32, p.cols, 8 * at(j), g);
       // padding rows, and lanes without a column (for the amax): (0 0) gamma = 0
-      const float rl = full || (live && at(j) < nv) ? rstd : 0.0f;
+      const float rl = FULL || (live && at(j) < nv) ? rstd : 0.0f;
       const float2 r2 = make_float2(rl, rl);
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[j][k] = __fmul2_rn(__fmul2_rn(x[j][k], r2), g[k]);
@@ -246,11 +241,14 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
 #pragma unroll
       for (int k = 0; k < 4; ++k) y[k] = x[j][k];
     };
-    if (full)
-      norm_row_copy<V, OUT, true>(p, y_of, r, live, stored, lane, at, tensor_scale, first, amax);
-    else
-      norm_row_copy<V, OUT, false>(p, y_of, r, live, stored, lane, at, tensor_scale, first, amax);
+    norm_row_copy<V, OUT, FULL>(p, y_of, r, live, stored, lane, at, tensor_scale, first, amax);
+  };
+  // (all warps of a group make the same rows, whichever form of the step they run, for they meet at
+  // its barriers)
+  if (whole) {
+    for (; r < rows; r += row_step) one_row(std::true_type{});
   }
+  for (; r - grp < rows_pad; r += row_step) one_row(std::false_type{});
   if constexpr (OUT == N_STATS || OUT == N_TENSOR) {
     if (p.part != nullptr) {
       const uint32_t m = cta_max(amax, redm);

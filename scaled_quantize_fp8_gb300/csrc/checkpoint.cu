@@ -2,9 +2,9 @@
 // (fp8_checkpoint_write), read back (fp8_checkpoint_read), and made into the FP8 copies that the
 // linear layer reads, with the norm in front of it or without (fp8_checkpoint_quantize).
 //
-// The first two are one pass over memory, 3 + 1/32 bytes an element. A thread has 16 columns (32 bytes of
-// bf16, 16 of codes); two lanes share a block's scale, eight a word of scales, so a row counts as a
-// whole number of 128 columns and the lanes beyond its end idle.
+// The first two are one pass over memory, 3 + 1/32 bytes an element. A thread has 16 columns (32
+// bytes of bf16, 16 of codes); two lanes share a block's scale, eight a word of scales, so a row
+// counts as a whole number of 128 columns and the lanes beyond its end idle.
 #include <algorithm>
 
 #include "ckpt.cuh"
@@ -21,6 +21,7 @@ struct CkptParams {
   int64_t ldx, units;         // units: rows * units of a row
   int cols, row_units;        // units of a row: 16 columns each, a multiple of 8
   int step_rows, step_units;  // a CTA's threads in rows and units
+  int v8;                     // x is 32-byte aligned (256-bit stores)
 };
 
 constexpr int kCkptThreads = 256;
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(kCkptThreads)
     if (at + i * kCkptThreads >= p.units || 16 * a.unit >= p.cols) continue;
     const float s = ckpt_factor(e[i]);
     const float2 s2 = make_float2(s, s);
-    uint4* x = reinterpret_cast<uint4*>(p.x + a.row * p.ldx + 16 * a.unit);
+    uint4 x[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       float2 f[4];
@@ -109,93 +110,119 @@ __global__ void __launch_bounds__(kCkptThreads)
       x[k] = make_uint4(pack_bf16(f[0].x, f[0].y), pack_bf16(f[1].x, f[1].y),
                         pack_bf16(f[2].x, f[2].y), pack_bf16(f[3].x, f[3].y));
     }
+    store_seg32(p.x + a.row * p.ldx + 16 * a.unit, x[0], x[1], true, true, p.v8);
   }
 }
 
 // The row copy of y = (h rstd) gamma (or of h) with h from its checkpoint, or, for per-tensor scales,
 // the partials of y's amax; padding rows are zeros. The column copy is the norm's column kernel's.
-// The threads of a CTA lie as in the kernels above; the CTAs stay and walk the units.
+// `width` lanes (8, 16 or 32) lie side by side on a row's units and stay on them, so gamma stays in
+// registers; the CTA walks its share of the rows, four of a thread's at a time, whose loads are all
+// issued first. (Threads that walk units of all columns: XX us more at 8192 x 4096.)
 template <int OUT>
-__global__ void __launch_bounds__(kCkptThreads)
-    checkpoint_row_kernel(const __grid_constant__ NormParams p) {
+__global__ void __launch_bounds__(kCkptThreads, 3)
+    checkpoint_row_kernel(const __grid_constant__ NormParams p, const int width,
+                          const uint32_t share) {
   __shared__ uint32_t red[kCkptThreads / 32];
   pdl_wait();
-  const uint32_t row_units = (p.cols + 127) / 128 * 8;
-  // less than 2^30, and a multiple of 32 (padded rows come by 16): whole warps
-  const uint32_t units = uint32_t(p.rows_pad) * row_units, step = gridDim.x * kCkptThreads;
-  const float tensor_scale = OUT == N_TENSOR ? *p.scale_in : 1.0f;
-  uint32_t amax = 0;
-  for (uint32_t at = blockIdx.x * kCkptThreads + threadIdx.x; at < units; at += step) {
-    const int64_t r = at / row_units;
-    const int unit = int(at % row_units), c = 16 * unit;
-    const bool in = c < p.cols, live = in && r < p.rows;
-    float2 y[2][4];
-    if (live) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.ck + r * p.cols + c));
-      const float e = ckpt_factor(__ldg(p.ck_scale + r * ckpt_pitch(p.cols) + (unit >> 1)));
-      const float f = p.rstd == nullptr ? e : e * p.rstd[r];
-      const float2 f2 = make_float2(f, f);
+  const uint32_t rows = uint32_t(p.rows), pitch = (p.cols + 127) / 128 * 4;
+  const uint32_t unit = blockIdx.x * width + threadIdx.x % width, c = 16 * unit;
+  const uint32_t step = kCkptThreads / width;        // rows side by side
+  const uint32_t begin = blockIdx.y * share + threadIdx.x / width;
+  // (padded rows come by 16, a warp has at most four of them: it ends as a whole)
+  const uint32_t end = min(uint32_t(p.rows_pad), (blockIdx.y + 1) * share);
+  const bool in = c < uint32_t(p.cols);
+  float2 g[2][4];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        ckpt_widen8(k == 0 ? make_uint2(v.x, v.y) : make_uint2(v.z, v.w), y[k]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[k][i] = __fmul2_rn(y[k][i], f2);
-        if (p.gamma != nullptr) {
-          float2 g[4];
-          gamma_pairs(p.gamma, p.gamma_fp32, p.cols, c + 8 * k, g);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) y[k][i] = __fmul2_rn(y[k][i], g[i]);
-        }
-      }
+  for (int k = 0; k < 2; ++k) {
+    if (p.gamma != nullptr) {
+      gamma_pairs(p.gamma, p.gamma_fp32, p.cols, c + 8 * k, g[k]);
     } else {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[k][i] = make_float2(0.0f, 0.0f);
+      for (int q = 0; q < 4; ++q) g[k][q] = make_float2(1.0f, 1.0f);
     }
-    uint32_t m = max(__float_as_uint(max8_abs(y[0])), __float_as_uint(max8_abs(y[1])));
-    if constexpr (OUT == N_STATS || OUT == N_TENSOR) amax = max(amax, m);
-    if constexpr (OUT != N_STATS) {
-      float s = tensor_scale;
-      if constexpr (OUT == N_MX) {
-        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        uint32_t w = mx_scale_byte_f32(m, &s) << (4 * (threadIdx.x & 6));
-        w |= __shfl_xor_sync(0xffffffffu, w, 2);
-        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        if ((unit & 7) == 0)
-          *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
-                                       mx_scale_offset32(uint32_t(r), unit >> 1, p.cols)) = w;
-      }
-      if constexpr (OUT == N_BW) {
+  }
+  const float tensor_scale = OUT == N_TENSOR ? *p.scale_in : 1.0f;
+  uint32_t amax = 0;
+  for (uint32_t r0 = begin; r0 < end; r0 += kCkptUnits * step) {
+    uint4 codes[kCkptUnits];
+    uint32_t bytes[kCkptUnits];
+    float rstd[kCkptUnits];
 #pragma unroll
-        for (int o = 1; o < 8; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float sinv;
-        s = scale_from_amax(__uint_as_float(m), p.margin, &sinv, 448.0f, p.pow2);
-        if ((unit & 7) == 0) {
-          if (p.pow2)
+    for (int i = 0; i < kCkptUnits; ++i) {
+      const uint32_t r = r0 + i * step;
+      codes[i] = make_uint4(0, 0, 0, 0);             // beyond the tensor: zeros
+      bytes[i] = 0;
+      rstd[i] = 0.0f;
+      if (in && r < min(rows, end)) {
+        codes[i] = __ldg(reinterpret_cast<const uint4*>(p.ck + uint64_t(r) * p.cols + c));
+        bytes[i] = __ldg(p.ck_scale + uint64_t(r) * pitch + (unit >> 1));
+        rstd[i] = p.rstd == nullptr ? 1.0f : p.rstd[r];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kCkptUnits; ++i) {
+      const uint32_t r = r0 + i * step;
+      if (r >= end) break;
+      float2 y[2][4];
+      const float f = ckpt_factor(bytes[i]) * rstd[i];
+      const float2 f2 = make_float2(f, f);
+      const bool live = r < rows;                    // else +0, whatever gamma's sign
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        ckpt_widen8(
+            k == 0 ? make_uint2(codes[i].x, codes[i].y) : make_uint2(codes[i].z, codes[i].w), y[k]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          y[k][q] = __fmul2_rn(__fmul2_rn(y[k][q], f2), g[k][q]);
+          if (!live) y[k][q] = make_float2(0.0f, 0.0f);
+        }
+      }
+      uint32_t m = max(__float_as_uint(max8_abs(y[0])), __float_as_uint(max8_abs(y[1])));
+      if constexpr (OUT == N_STATS || OUT == N_TENSOR) amax = max(amax, m);
+      if constexpr (OUT != N_STATS) {
+        float s = tensor_scale;
+        if constexpr (OUT == N_MX) {
+          m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          uint32_t w = mx_scale_byte_f32(m, &s) << (4 * (threadIdx.x & 6));
+          w |= __shfl_xor_sync(0xffffffffu, w, 2);
+          w |= __shfl_xor_sync(0xffffffffu, w, 4);
+          if ((unit & 7) == 0 && in)
             *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
-                                         mx_scale_offset32(uint32_t(r), unit >> 1, p.cols)) =
-                e8m0_of_pow2(sinv) * 0x01010101u;
-          else
-            reinterpret_cast<float*>(p.row_scale)[int64_t(unit >> 3) * p.rows_pad + r] = sinv;
+                                         mx_scale_offset32(r, unit >> 1, p.cols)) = w;
         }
-      }
-      if (in) {
-        const float2 s2 = make_float2(s, s);
-        uint32_t w[4];
+        if constexpr (OUT == N_BW) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 a = __fmul2_rn(y[k >> 1][2 * (k & 1)], s2);
-          const float2 b = __fmul2_rn(y[k >> 1][2 * (k & 1) + 1], s2);
-          w[k] = cvt_e4m3x4(a.x, a.y, b.x, b.y);
+          for (int o = 1; o < 8; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          float sinv;
+          s = scale_from_amax(__uint_as_float(m), p.margin, &sinv, 448.0f, p.pow2);
+          if ((unit & 7) == 0 && in) {
+            if (p.pow2)
+              *reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(p.row_scale) +
+                                           mx_scale_offset32(r, unit >> 1, p.cols)) =
+                  e8m0_of_pow2(sinv) * 0x01010101u;
+            else
+              reinterpret_cast<float*>(p.row_scale)[int64_t(unit >> 3) * p.rows_pad + r] = sinv;
+          }
         }
-        *reinterpret_cast<uint4*>(p.row + r * p.cols + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (in) {
+          const float2 s2 = make_float2(s, s);
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 a = __fmul2_rn(y[k >> 1][2 * (k & 1)], s2);
+            const float2 b = __fmul2_rn(y[k >> 1][2 * (k & 1) + 1], s2);
+            w[k] = cvt_e4m3x4(a.x, a.y, b.x, b.y);
+          }
+          *reinterpret_cast<uint4*>(p.row + uint64_t(r) * p.cols + c) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
     }
   }
   if constexpr (OUT == N_STATS || OUT == N_TENSOR) {
     const uint32_t m = cta_max(amax, red);
-    if (threadIdx.x == 0) p.part[blockIdx.x] = m;
+    if (threadIdx.x == 0) p.part[blockIdx.y * gridDim.x + blockIdx.x] = m;
   }
   pdl_launch_dependents();
 }
@@ -204,15 +231,22 @@ namespace {
 
 cudaError_t checkpoint_rows(int out_kind, const NormParams& p, const void*, int* ctas,
                             cudaStream_t st) {
-  const int64_t units = p.rows_pad * ((p.cols + 127) / 128 * 8);
-  const unsigned grid = unsigned(std::min<int64_t>((units + kCkptThreads - 1) / kCkptThreads,
-                                                   int64_t(num_sms()) * 8));
-  if (ctas != nullptr) *ctas = int(grid);
+  const int row_units = (p.cols + 127) / 128 * 8;
+  const int width = row_units >= 32 ? 32 : row_units == 16 ? 16 : 8;
+  const unsigned blocks = (row_units + width - 1) / width;
+  // the rows in as many shares as make three CTAs an SM, each some steps of all its threads
+  const int64_t quantum = kCkptThreads / width * kCkptUnits;
+  const int64_t shares = std::max<int64_t>(
+      1, std::min<int64_t>((p.rows_pad + quantum - 1) / quantum, num_sms() * 3 / blocks));
+  const int64_t share = ((p.rows_pad + shares - 1) / shares + quantum - 1) / quantum * quantum;
+  const unsigned used = unsigned((p.rows_pad + share - 1) / share);
+  if (ctas != nullptr) *ctas = int(blocks * used);
   auto kern = out_kind == N_MX       ? checkpoint_row_kernel<N_MX>
               : out_kind == N_BW     ? checkpoint_row_kernel<N_BW>
               : out_kind == N_TENSOR ? checkpoint_row_kernel<N_TENSOR>
                                      : checkpoint_row_kernel<N_STATS>;
-  return launch_kernel(kern, dim3(grid), dim3(kCkptThreads), 0, st, nullptr, p);
+  return launch_kernel(kern, dim3(blocks, used), dim3(kCkptThreads), 0, st, nullptr, p, width,
+                       uint32_t(share));
 }
 
 CkptParams ckpt_params(const uint16_t* x, int64_t ldx, int64_t rows, int64_t cols,
@@ -225,6 +259,7 @@ CkptParams ckpt_params(const uint16_t* x, int64_t ldx, int64_t rows, int64_t col
   p.cols = int(cols);
   p.row_units = int((cols + 127) / 128 * 8);
   p.units = rows * p.row_units;
+  p.v8 = reinterpret_cast<uintptr_t>(x) % 32 == 0;    // (columns come by 16)
   p.step_rows = kCkptThreads / p.row_units;
   p.step_units = kCkptThreads % p.row_units;
   *grid = unsigned((p.units + kCkptThreads * kCkptUnits - 1) / (kCkptThreads * kCkptUnits));

@@ -261,6 +261,12 @@ struct NormColSmem<true> {
   uint32_t red[4];
 };
 
+// A row's rstd and the E8M0 bytes of a tile's two blocks.
+struct CkptRow {
+  float rstd;
+  uint32_t bytes;
+};
+
 // FULL: nothing but the FP8 column copy is wanted and every tile lies inside the padded tensor,
 // so nothing is tested per row (8192 x 4096, both copies: 48.7 us, else 52.6, with a few spills).
 // CK: h comes from its checkpoint (fp8_checkpoint_quantize).
@@ -294,11 +300,13 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
                                     n ? p.ck + (r0 + row) * p.cols + cp : p.ck, n, first);
       }
       ptx::cp_async_commit();
-      if (r0 + t >= p.rows) return make_float2(0.0f, 0.0f);
-      const uint32_t e = *reinterpret_cast<const uint16_t*>(
-          p.ck_scale + (r0 + t) * ckpt_pitch(p.cols) + (c0 >> 5));
-      const float rs = p.rstd == nullptr ? 1.0f : p.rstd[r0 + t];
-      return make_float2(ckpt_factor(e & 0xFFu) * rs, ckpt_factor(e >> 8) * rs);
+      CkptRow v = {0.0f, 0u};                         // as loaded: nothing waits for it here
+      if (r0 + t < p.rows) {
+        v.bytes = *reinterpret_cast<const uint16_t*>(p.ck_scale + (r0 + t) * ckpt_pitch(p.cols) +
+                                                     (c0 >> 5));
+        v.rstd = p.rstd == nullptr ? 1.0f : p.rstd[r0 + t];
+      }
+      return v;
     } else {
       // thread t copies piece t % 8 of the rows t / 8, t / 8 + 16, ..
       const int64_t r0 = int64_t(tile) * 128, r = r0 + (t >> 3);
@@ -356,8 +364,8 @@ __global__ void __launch_bounds__(128, col_ctas<OUT, FULL>())
   for (int buf = 0; tile >= 0; tile -= step, buf ^= 1) {
     const int64_t r0 = int64_t(tile) * 128, r = r0 + 8 * l16;
     if constexpr (CK) {
-      S.rstd[buf][0][t] = next_rstd.x;
-      S.rstd[buf][1][t] = next_rstd.y;
+      S.rstd[buf][0][t] = ckpt_factor(next_rstd.bytes & 0xFFu) * next_rstd.rstd;
+      S.rstd[buf][1][t] = ckpt_factor(next_rstd.bytes >> 8) * next_rstd.rstd;
     } else {
       S.rstd[buf][t] = next_rstd;
     }
