@@ -266,7 +266,14 @@ cudaError_t launch_branch(const NormParams& n, const BranchParams& more, int* ct
                           cudaStream_t st) {
   BranchParams b = more;
   b.n = n;
-  const RowPlan pl = row_plan(n.cols, 4, 384);
+  // Two vectors a thread up to 4096 columns, four beyond: us with two / four
+  //   1 x 4096, row copy                     4.1 /  6.4
+  //   8192 x 4096, row copy                 41.2 / 42.6     with checkpoints 54.4 / 56.0
+  //   8192 x 4096, both copies              57.0 / 55.8     with checkpoints 70.3 / 68.8
+  //   8192 x 5120, both, with checkpoints  103.7 / 86.0
+  // A row's sums, and so its last bits, must not depend on how many rows there are: the rule goes by
+  // the columns alone.
+  const RowPlan pl = row_plan(n.cols, n.cols <= 4096 ? 2 : 4, n.cols <= 4096 ? 256 : 384);
   const int rpc = pl.block / pl.tpr;
   auto kern = pl.v == 1   ? branch_row_kernel<1, OUT>
               : pl.v == 2 ? branch_row_kernel<2, OUT>
