@@ -603,8 +603,8 @@ typedef struct {
   float *dtoken_gate;        /* [rows]; NULL without token_gate */
 } fp8_branch_grad_out;
 
-/* Bytes of scratch fp8_branch_rmsnorm_bwd needs (0 when none of dgamma, dgamma_post and dgate is
- * wanted). */
+/* Bytes of scratch fp8_branch_rmsnorm_bwd needs for dgamma, dgamma_post and dgate (none where none of
+ * them is wanted). */
 size_t fp8_branch_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
 
 /*

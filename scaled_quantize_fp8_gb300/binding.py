@@ -639,16 +639,14 @@ def rmsnorm_bwd(dy: torch.Tensor, h: "torch.Tensor | Checkpoint", rstd: torch.Te
 
 def _one_device(*tensors):
     """Every tensor (or None) of a call on the current device, where its kernels run."""
-    here = torch._C._cuda_getDevice() if tensors[0].is_cuda else -1
+    if not tensors[0].is_cuda:
+        _not_on_gpu()
+    here = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != here:
-            _not_on_gpu() if not t.is_cuda else _other_device()
-    if here < 0:
-        _not_on_gpu()
-
-
-def _other_device():
-    raise ValueError("the tensors of a call lie on the current device")
+            if not t.is_cuda:
+                _not_on_gpu()
+            raise ValueError("the tensors of a call lie on the current device")
 
 
 def _columns(t: Optional[torch.Tensor], cols, name: str):
@@ -798,8 +796,8 @@ def branch_rmsnorm_quantize(recipe: Optional[Recipe], branch: torch.Tensor,
                               token_ptr, gamma.data_ptr(), ld_branch, ld_residual, rows, cols,
                               post_fp32, gate_fp32, _gamma(gamma, cols), scale,
                               eps if eps_post is None else eps_post, eps)
-    _one_device(*tensors)
     rc = out_ref = None
+    on_gpu = True
     if want_row or want_col:
         block = recipe.kind in ("mxfp8", "blockwise")
         q = 128 if block else 16
@@ -809,10 +807,11 @@ def branch_rmsnorm_quantize(recipe: Optional[Recipe], branch: torch.Tensor,
                 out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
                                     device=branch.device)
         ct, on_gpu = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
-        if not on_gpu:
-            _not_on_gpu()
         fields = recipe._fields()
         out_ref, rc = ctypes.byref(ct), L.pack_recipe(*fields)
+    _one_device(*tensors)
+    if not on_gpu:
+        _not_on_gpu()
     args = (rc, inp, want_row, want_col, h.data_ptr(),
             None if rstd_branch is None else rstd_branch.data_ptr(), rstd.data_ptr(),
             None if y is None else y.data_ptr(), o_ck, h_ck, out_ref)
@@ -850,7 +849,6 @@ def checkpoint_quantize(recipe: Recipe, ck: Checkpoint, rstd: Optional[torch.Ten
     if rstd is not None:
         _like(rstd, (rows,), _FP32, "rstd")
         gamma_fp32 = _gamma(gamma, cols)
-    _one_device(ck.codes, ck.scale, rstd, gamma, workspace)
     block = recipe.kind in ("mxfp8", "blockwise")
     q = 128 if block else 16
     padded = -(-rows // q) * q
@@ -859,6 +857,7 @@ def checkpoint_quantize(recipe: Recipe, ck: Checkpoint, rstd: Optional[torch.Ten
             out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
                                 device=ck.codes.device)
     ct, on_gpu = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
+    _one_device(ck.codes, ck.scale, rstd, gamma, workspace)
     if not on_gpu:
         _not_on_gpu()
     fields = recipe._fields()
@@ -962,24 +961,23 @@ def branch_rmsnorm_bwd(dy: torch.Tensor, h: "torch.Tensor | Checkpoint", rstd: t
                              gate_ptr, token_ptr, gamma.data_ptr(), ro_ptr, rstd.data_ptr(),
                              _rows_2d(dy, cols, "dy"), ld_dres, ld_h, ld_o, rows, cols, post_fp32,
                              gate_fp32, _gamma(gamma, cols), scale)
-    device = dy.device
+    device, vector = dy.device, (cols,)
 
-    def made(t, shape, dtype, name, wanted=True):
-        if not wanted:
-            return None
+    def made(t, shape, dtype, name):
         if t is None:
             t = _empty(shape, dtype, device, stream)
-        else:
+        elif t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             _like(t, shape, dtype, name)
         tensors.append(t)
         return t
 
     out = BranchGrads(
         made(dh, shape, _BF16, "dh"), made(dbranch, shape, _BF16, "dbranch"),
-        made(dgamma, (cols,), _FP32, "dgamma", want_dgamma),
-        made(dgamma_post, (cols,), _FP32, "dgamma_post", want_dgamma and gamma_post is not None),
-        made(dgate, (cols,), _FP32, "dgate", want_dgamma and gate is not None),
-        made(dtoken_gate, (rows,), _FP32, "dtoken_gate", token_gate is not None))
+        made(dgamma, vector, _FP32, "dgamma") if want_dgamma else None,
+        made(dgamma_post, vector, _FP32, "dgamma_post")
+        if want_dgamma and gamma_post is not None else None,
+        made(dgate, vector, _FP32, "dgate") if want_dgamma and gate is not None else None,
+        made(dtoken_gate, (rows,), _FP32, "dtoken_gate") if token_gate is not None else None)
     _one_device(*tensors)
     args = (inp, L.pack_branch_grad_out(*[0 if t is None else t.data_ptr() for t in out]))
     rest = (None if status is None else status.data_ptr(), _raw_stream(stream))

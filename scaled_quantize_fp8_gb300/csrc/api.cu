@@ -692,6 +692,9 @@ fp8_status check_vector(const void* p, int32_t fp32) {
 
 bool finite(float v) { return v - v == 0.0f; }
 
+// Two outputs that are one buffer (both given).
+bool same(const void* a, const void* b) { return a != nullptr && a == b; }
+
 fp8_status check_checkpoint(const fp8_checkpoint* c) {
   FP8_TRY(check_ptr(c->codes));
   return check_ptr(c->scale);
@@ -917,6 +920,10 @@ fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_branc
       return FP8_ERR_ALIGN;
     if (branch_ckpt != nullptr) FP8_TRY(check_checkpoint(branch_ckpt));
     if (h_ckpt != nullptr) FP8_TRY(check_checkpoint(h_ckpt));
+    if (same(rstd, rstd_branch) || same(h_bf16, y_bf16) ||
+        (branch_ckpt != nullptr && h_ckpt != nullptr &&
+         (branch_ckpt->codes == h_ckpt->codes || branch_ckpt->scale == h_ckpt->scale)))
+      return FP8_ERR_SHAPE;                 // one buffer for two outputs
   }
   set_norm_out(a, out);
   if (empty) return empty_norm(a, want_row, want_col, out, workspace, stream);
@@ -975,7 +982,9 @@ fp8_status fp8_branch_rmsnorm_bwd(const fp8_branch_grad* in, const fp8_branch_gr
   FP8_TRY(check_floats(in->token_gate));
   FP8_TRY(check_ptr(out->dh));
   FP8_TRY(check_ptr(out->dbranch));
-  if (out->dh == out->dbranch) return FP8_ERR_SHAPE;
+  if (out->dh == out->dbranch || same(out->dgamma, out->dgamma_post) ||
+      same(out->dgamma, out->dgate) || same(out->dgamma_post, out->dgate))
+    return FP8_ERR_SHAPE;                   // one buffer for two outputs
   for (const void* d : {out->dh, out->dbranch}) {     // in place only where the rows lie alike
     if ((d == in->dy && in->ld_dy != cols) || (d == in->dres && in->ld_dres != cols) ||
         (!h_ckpt && d == in->h && in->ld_h != cols) ||
