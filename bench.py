@@ -1031,7 +1031,8 @@ def run_reference(args):
 
 def norm_cases(torch, F):
     """The norm's and the gradients' kernels at the MLP's sizes: name -> (one launch, bytes that it
-    has to move). x or residual, h, row and column copy; dy, h, dres, dh; the gradients twice."""
+    has to move). x or residual, h, row and column copy; dy, h, dres, dh; the gradients twice; with
+    checkpoints, 1 + 1/32 bytes an element for each that is read or written."""
     M, K, Fd = TOKENS, HIDDEN, FFN
     g = torch.Generator(device="cuda").manual_seed(0)
 
@@ -1056,6 +1057,27 @@ def norm_cases(torch, F):
     cases["norm_mxfp8"][0]()                                  # h and rstd
     cases["norm_bwd"] = (lambda: F.rmsnorm_bwd(dy, h, rstd, gamma, dres=res, dh=dh, dgamma=dgamma,
                                                workspace=ws), M * K * 8)
+    # the gated branch with norms before and after it, its checkpoints, and what reads them
+    rec, ck, scale_bytes = F.Recipe(kind="mxfp8"), 1 + 1 / 32.0, 1 / 32.0
+    gate, ro, do = randn(K), torch.ones_like(rstd), torch.empty_like(x)
+    out, h_ck, o_ck = F.empty_qtensor(rec, M, K, "activation"), F.checkpoint(x), F.checkpoint(res)
+    fws = torch.empty(F.rmsnorm_workspace_bytes(rec, M, K), dtype=torch.uint8, device="cuda")
+    bws = torch.empty(F.branch_rmsnorm_bwd_workspace_bytes(M, K), dtype=torch.uint8, device="cuda")
+    dpost, dgate = torch.empty_like(dgamma), torch.empty_like(dgamma)
+    cases["branch_mxfp8"] = (lambda: F.branch_rmsnorm_quantize(
+        rec, x, res, gamma, gamma_post=gamma, gate=gate, scale=0.2, out=out, h=h, rstd=rstd,
+        rstd_branch=ro, branch_ckpt=o_ck, h_ckpt=h_ck, workspace=fws),
+        M * K * (8 + 2 * scale_bytes + 2 * ck))
+    cases["branch_bwd"] = (lambda: F.branch_rmsnorm_bwd(
+        dy, h_ck, rstd, gamma, o_ck, rstd_branch=ro, gamma_post=gamma, gate=gate, scale=0.2,
+        dres=res, dh=dh, dbranch=do, dgamma=dgamma, dgamma_post=dpost, dgate=dgate,
+        workspace=bws), M * K * (8 + 2 * ck))
+    cases["norm_bwd_checkpoint"] = (lambda: F.rmsnorm_bwd(
+        dy, h_ck, rstd, gamma, dres=res, dh=dh, dgamma=dgamma, workspace=ws), M * K * (6 + ck))
+    cases["checkpoint_write"] = (lambda: F.checkpoint(x, out=h_ck), M * K * (2 + ck))
+    cases["checkpoint_read"] = (lambda: F.checkpoint_read(h_ck, out=do), M * K * (2 + ck))
+    cases["checkpoint_quantize"] = (lambda: F.checkpoint_quantize(
+        rec, h_ck, rstd, gamma, out=out, workspace=fws), M * K * (3 * ck))
     grads = [randn(Fd, K, dtype=torch.float32), randn(K, Fd, dtype=torch.float32)]
     grads = F.GradList(grads, [torch.empty_like(t) for t in grads])   # in place: clipped once only
     gws = torch.empty(F.grad_workspace_bytes(2), dtype=torch.uint8, device="cuda")
@@ -1084,7 +1106,11 @@ def run_profile_case(args):
     blockwise recipe (X in 1x128 blocks, W1 and W2 in 128x128 tiles).
     norm_mx / norm_tensorwise / norm_blockwise / norm_delayed: RMSNorm with a residual and both
     FP8 copies, 8192 x 4096; norm_bwd: its backward pass; grad: gradient norm, then clipping, of
-    the fp32 gradients of the MLP's two weights (134M elements)."""
+    the fp32 gradients of the MLP's two weights (134M elements).
+    branch_mx: a gated branch with norms before and after it, both MXFP8 copies and two 8-bit
+    checkpoints, 8192 x 4096; branch_bwd: its backward pass from the checkpoints;
+    norm_bwd_checkpoint: the norm's from one; checkpoint_write / checkpoint_read /
+    checkpoint_quantize (both MXFP8 copies of the norm made again)."""
     import torch
     import scaled_quantize_fp8_gb300 as F
     from scaled_quantize_fp8_gb300 import build as B
@@ -1149,7 +1175,7 @@ def run_profile_case(args):
         dw = torch.empty((4096, 4096), dtype=torch.bfloat16, device="cuda")
         for _ in range(args.steps):
             F.linear_bwd(rec, dyq, xq, None, want_dx=False, dw=dw)
-    elif case.startswith("norm") or case == "grad":
+    elif case.startswith(("norm", "branch", "checkpoint")) or case == "grad":
         run = norm_cases(torch, F)[case.replace("_mx", "_mxfp8")][0]
         for _ in range(args.steps):
             run()
@@ -1386,7 +1412,9 @@ def main():
                              "gemm_tensorwise", "gemm_blockwise", "gelu_mx", "dgelu_mx",
                              "gemm_gelu_mx", "gemm_dgelu_mx", "gemm_mx_mlp",
                              "gemm_wgrad_blockwise", "norm_mx", "norm_tensorwise",
-                             "norm_blockwise", "norm_delayed", "norm_bwd", "grad", "suite"])
+                             "norm_blockwise", "norm_delayed", "norm_bwd", "grad", "branch_mx",
+                             "branch_bwd", "norm_bwd_checkpoint", "checkpoint_write",
+                             "checkpoint_read", "checkpoint_quantize", "suite"])
     ap.add_argument("--rows", type=int, default=16384, help="--profile quant_*: tensor rows")
     ap.add_argument("--cols", type=int, default=8192, help="--profile quant_*: tensor columns")
     ap.add_argument("--gpus", type=int, default=1)

@@ -10,6 +10,14 @@
 // the same columns in all of its rows and adds dgamma and S for them in registers. The CTAs' sums
 // go to the workspace and branch_sums_kernel adds them in a fixed order. dh goes on in fp32: its
 // rounding to bf16 is the output's alone.
+//
+// 8192 x 4096 from both checkpoints, with dres, moves 338 MB: 61.4 us (49.8 at a copy's rate), of
+// which branch_sums_kernel about 3; from bf16 403 MB in 67.0 (59.4). What bounds it: 16 warps an SM,
+// by registers, for rows that are chains of two sums; 36 instructions an element from checkpoints
+// (29 from bf16). A CTA of three groups with four vectors and 168 registers a thread took 121. Wide
+// rows have one group an SM and nothing beside it: 4096 x 8192 66.5 us, 8192 x 5120 105 (62), 2048 x
+// 16384 (clusters of two) 117, 1024 x 32768 (of four) 207; with four vectors a thread in one CTA
+// the last two took 182 and more.
 #include <algorithm>
 #include <type_traits>
 
@@ -62,10 +70,12 @@ __host__ __device__ constexpr int bwd_row_bytes() {      // of a thread
 }
 
 // tpr threads per row (16, or whole warps), V vectors of eight columns a thread, laid out as in
-// branch_row_kernel. Every thread copies its own elements
-// of the next row to its own slots of shared memory while it works on the present one, and reads
-// them once for each of the row's three steps: mean(a xh); dh and s; do. Only dh stays in
-// registers in between.
+// branch_row_kernel. Every thread copies its own elements of the next row to its own slots of shared
+// memory while it works on the present one, whose three steps, mean(a xh), dh and s, and do, it
+// makes in the same registers. rstd and rstd_o, and a checkpoint's powers of two, are factors of
+// whole vectors: they are applied to a vector's sums and to its other factors, not to its elements
+// (69.7 us -> 65.1 with dy, h and o kept in registers), and whole warps run a form of the row's step
+// in which nothing is tested (-> 61.4).
 // CL: a row of more than 8192 columns, whose two column sums a thread no longer fit in the registers
 // of one CTA, lies in the two or four CTAs of a cluster, each of which adds the others' parts of the
 // row's sums, which arrive in shared memory.
