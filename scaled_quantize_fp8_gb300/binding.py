@@ -596,7 +596,7 @@ def rmsnorm_bwd(dy: torch.Tensor, h: "torch.Tensor | Checkpoint", rstd: torch.Te
             raise ValueError("dres: the shape of h")
         ld_dres, dres_ptr = _rows_2d(dres, cols, "dres"), dres.data_ptr()
     ck = None
-    if type(h) is Checkpoint:
+    if isinstance(h, Checkpoint):
         ck = _checkpoint(h, shape, "h")
         _one_device(dy, h.codes, h.scale, rstd, gamma, dres, dh, dgamma, workspace)
         h, ld_h = h.codes, cols
@@ -926,14 +926,14 @@ def branch_rmsnorm_bwd(dy: torch.Tensor, h: "torch.Tensor | Checkpoint", rstd: t
     none = (0, 0)
     h_ptr = o_ptr = ld_h = ld_o = 0
     h_ck = o_ck = none
-    if type(h) is Checkpoint:
+    if isinstance(h, Checkpoint):
         _checkpoint(h, shape, "h")
         h_ck = (h.codes.data_ptr(), h.scale.data_ptr())
         tensors += (h.codes, h.scale)
     else:
         h_ptr, ld_h = h.data_ptr(), _rows_2d(h, cols, "h")
         tensors.append(h)
-    if type(branch) is Checkpoint:
+    if isinstance(branch, Checkpoint):
         _checkpoint(branch, shape, "branch")
         o_ck = (branch.codes.data_ptr(), branch.scale.data_ptr())
         tensors += (branch.codes, branch.scale)

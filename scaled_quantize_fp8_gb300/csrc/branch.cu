@@ -12,11 +12,11 @@
 //
 // 8192 x 4096 with both MXFP8 copies and both checkpoints has to move 340 MB, 50.0 us at the 6791
 // GB/s of a copy; the two kernels take 70.7, the row kernel alone (305 MB, 44.9) 54.3, 0.83 of that
-// rate. What bounds it: the row kernel's time does not follow its instructions (28 to 41 an element,
-// all within 3 us) nor the loads in flight; half of its stalls are for shuffles and shared memory,
-// its warps (24 an SM, by registers) go through two sums of a row with a barrier each. The column
-// kernel adds 16 us, in which the lines that the row kernel left in L2 are written too. The two side
-// by side (on two streams, of different tensors) took as long as in turn, 69 us.
+// rate. What bounds it: the row kernel's time does not follow its instructions (28 to 41 an
+// element, all within 3 us) nor the loads in flight; half of its stalls are for shuffles and shared
+// memory, its warps (24 an SM, by registers) go through two sums of a row with a barrier each. The
+// column kernel adds 16 us, in which the lines that the row kernel left in L2 are written too. The
+// two side by side (on two streams, of different tensors) took as long as in turn, 69 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -56,13 +56,6 @@ __host__ __device__ constexpr int branch_slot_bytes() {
 }
 __host__ __device__ constexpr int branch_vec_bytes(int v) { return v <= 4 ? v * 64 : 0; }
 
-// tpr threads a row (16, or whole warps); a warp's V vectors a lane follow each other, so that what
-// distinguishes them is a constant in every address: lane l of warp w has the units 32 (V w + j) + l.
-// (Four vectors a thread: 32 instructions an element, 39 with a thread's vectors tpr units apart.)
-// A row is a chain of two sums, with a barrier each, and every element is worked on about five times,
-// so instructions count as much as bytes: w and gamma lie in shared memory as floats, o, h and y
-// follow each other in the same registers, and whole warps run a form of the row's step in which
-// nothing is tested.
 // The L2 policies as values that may be made again where they are used (no registers kept).
 __device__ __forceinline__ uint64_t policy_first() {
   uint64_t p;
@@ -75,6 +68,13 @@ __device__ __forceinline__ uint64_t policy_last() {
   return p;
 }
 
+// tpr threads a row (16, or whole warps); a warp's V vectors a lane follow each other, so that what
+// distinguishes them is a constant in every address: lane l of warp w has the units 32 (V w + j) + l.
+// (Four vectors a thread: 32 instructions an element, 39 with a thread's vectors tpr units apart.)
+// A row is a chain of two sums, with a barrier each, and every element is worked on about five
+// times, so instructions count as much as bytes: w and gamma lie in shared memory as floats, o, h and
+// y follow each other in the same registers, and whole warps run a form of the row's step in which
+// nothing is tested.
 template <int V, int OUT>
 __global__ void __maxnreg__(V <= 4 ? 80 : 128)
     branch_row_kernel(const __grid_constant__ BranchParams b) {
@@ -280,8 +280,8 @@ cudaError_t launch_branch(const NormParams& n, const BranchParams& more, int* ct
   //   8192 x 4096, row copy                 41.2 / 42.6     with checkpoints 54.4 / 56.0
   //   8192 x 4096, both copies              57.0 / 55.8     with checkpoints 70.3 / 68.8
   //   8192 x 5120, both, with checkpoints  103.7 / 86.0
-  // A row's sums, and so its last bits, must not depend on how many rows there are: the rule goes by
-  // the columns alone.
+  // A row's sums, and so its last bits, must not depend on how many rows there are: the rule goes
+  // by the columns alone.
   const RowPlan pl = row_plan(n.cols, n.cols <= 4096 ? 2 : 4, n.cols <= 4096 ? 256 : 384);
   const int rpc = pl.block / pl.tpr;
   auto kern = pl.v == 1   ? branch_row_kernel<1, OUT>

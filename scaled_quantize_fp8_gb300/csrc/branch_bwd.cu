@@ -70,12 +70,12 @@ __host__ __device__ constexpr int bwd_row_bytes() {      // of a thread
 }
 
 // tpr threads per row (16, or whole warps), V vectors of eight columns a thread, laid out as in
-// branch_row_kernel. Every thread copies its own elements of the next row to its own slots of shared
-// memory while it works on the present one, whose three steps, mean(a xh), dh and s, and do, it
-// makes in the same registers. rstd and rstd_o, and a checkpoint's powers of two, are factors of
+// branch_row_kernel. Every thread copies its own elements of the next row to its own slots of
+// shared memory while it works on the present one, whose three steps, mean(a xh), dh and s, and do,
+// it makes in the same registers. rstd and rstd_o, and a checkpoint's powers of two, are factors of
 // whole vectors: they are applied to a vector's sums and to its other factors, not to its elements
-// (69.7 us -> 65.1 with dy, h and o kept in registers), and whole warps run a form of the row's step
-// in which nothing is tested (-> 61.4).
+// (69.7 us -> 65.1 with dy, h and o kept in registers), and whole warps run a form of the row's
+// step in which nothing is tested (-> 61.4).
 // CL: a row of more than 8192 columns, whose two column sums a thread no longer fit in the registers
 // of one CTA, lies in the two or four CTAs of a cluster, each of which adds the others' parts of the
 // row's sums, which arrive in shared memory.

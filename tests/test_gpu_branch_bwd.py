@@ -270,6 +270,26 @@ def test_equal_calls_give_equal_bits_on_any_stream_and_in_graphs():
         assert all(torch.equal(x, y) for x, y in zip(a, outs))
 
 
+@pytest.mark.parametrize("cols", [2064, 16400, 32768])
+def test_graph_of_ragged_and_wide_rows(cols):
+    """Groups with whole and ragged warps, and clusters, captured and replayed."""
+    c = case(37, cols, token=True)
+    ref = check(c)
+    dev = dict(dy=to_dev_bf16(c["dy"]), rstd=_cuda(c["rstd"]),
+               gamma=_dev_gamma(c["gamma"], False), rstd_branch=_cuda(c["ro"]),
+               gamma_post=_dev_gamma(c["a"], False), gate=_dev_gamma(c["g"], False),
+               token_gate=_cuda(c["t"]), dres=to_dev_bf16(c["dres"]))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        d = F.branch_rmsnorm_bwd(h=c["h"], branch=c["o"], scale=c["scale"], **dev)
+    for _ in range(2):
+        for t in d:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(ref, d))
+
+
 def test_offsets_past_32_bits():
     cols, rows = 32768, (1 << 31) // 32768 + 3
     x = torch.zeros((rows, cols), dtype=torch.bfloat16, device="cuda")
