@@ -11,12 +11,12 @@
 // backward pass reads. The column copy is made by the norm's column kernel from h, in L2.
 //
 // 8192 x 4096 with both MXFP8 copies and both checkpoints has to move 340 MB, 50.0 us at the 6791
-// GB/s of a copy; the two kernels take 70.7, the row kernel alone (305 MB, 44.9) 54.3, 0.83 of that
+// GB/s of a copy; the two kernels take 69.7, the row kernel alone (305 MB, 44.9) 52.9, 0.85 of that
 // rate. What bounds it: the row kernel's time does not follow its instructions (28 to 41 an
-// element, all within 3 us) nor the loads in flight; half of its stalls are for shuffles and shared
-// memory, its warps (24 an SM, by registers) go through two sums of a row with a barrier each. The
-// column kernel adds 16 us, in which the lines that the row kernel left in L2 are written too. The
-// two side by side (on two streams, of different tensors) took as long as in turn, 69 us.
+// element, all within 3 us); half of its stalls are for shuffles and shared memory, its warps (24
+// an SM, by registers) go through two sums of a row with a barrier each. The column kernel adds 17
+// us, in which the lines that the row kernel left in L2 are written too. The two side by side (on
+// two streams, of different tensors) took as long as in turn.
 #include <algorithm>
 #include <type_traits>
 
@@ -42,10 +42,12 @@ struct BranchParams {
   uint8_t* h_scale;
 };
 
-// Rows on their way while one is worked on.
+// Buffers for rows, of which what has been read of one takes in the row that comes next to it (o's
+// half as soon as o is read, the stream's later). With one vector two are faster, 65536 x 256: 39.3
+// us instead of 40.2 with four; else one: 8192 x 4096 69.9, two 72.4, two for whole rows 71.3.
 template <int V>
 __host__ __device__ constexpr int branch_ahead() {
-  return V == 1 ? 4 : V == 2 ? 2 : 1;
+  return V == 1 ? 2 : 1;
 }
 // Shared memory of a thread, for the rows on their way, and of a lane, for w and gamma of its
 // columns. A warp's pieces lie side by side (cp.async of lanes that write 144 bytes apart: 71 us
@@ -69,12 +71,12 @@ __device__ __forceinline__ uint64_t policy_last() {
 }
 
 // tpr threads a row (16, or whole warps); a warp's V vectors a lane follow each other, so that what
-// distinguishes them is a constant in every address: lane l of warp w has the units 32 (V w + j) + l.
-// (Four vectors a thread: 32 instructions an element, 39 with a thread's vectors tpr units apart.)
-// A row is a chain of two sums, with a barrier each, and every element is worked on about five
-// times, so instructions count as much as bytes: w and gamma lie in shared memory as floats, o, h and
-// y follow each other in the same registers, and whole warps run a form of the row's step in which
-// nothing is tested.
+// distinguishes them is a constant in every address: lane l of warp w has the units 32 (V w + j) +
+// l. (Four vectors a thread: 32 instructions an element, 39 with a thread's vectors tpr units
+// apart.) A row is a chain of two sums, with a barrier each, and every element is worked on about
+// five times, so instructions count as much as bytes: w and gamma lie in shared memory as floats, o,
+// h and y follow each other in the same registers, and whole warps run a form of the row's step in
+// which nothing is tested.
 template <int V, int OUT>
 __global__ void __maxnreg__(V <= 4 ? 80 : 128)
     branch_row_kernel(const __grid_constant__ BranchParams b) {
@@ -100,30 +102,33 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
   // (less than 2^31 rows, and as many threads at most beyond them)
   const uint32_t rows = uint32_t(p.rows), rows_pad = uint32_t(p.rows_pad), cols = p.cols;
   const uint32_t row_step = gridDim.x * rpc, r_first = blockIdx.x * rpc + grp;
-  const auto prefetch = [&](uint32_t r, int buf) {
-    uint4* s = slot + buf * (32 * 2 * V);
-    const uint16_t* x_next = p.x + uint64_t(r) * uint32_t(p.ldx) + 8 * at.first;
-    const uint16_t* res_next = p.res + uint64_t(r) * uint32_t(p.ldr) + 8 * at.first;
+  // Each thread copies its own elements of a row, o and res in groups of their own: what it has
+  // read of a buffer makes room for the row that comes next to it.
+  const auto prefetch = [&](uint32_t r, int buf, auto res_tag) {
+    constexpr bool RES = decltype(res_tag)::value;
+    uint4* s = slot + buf * (32 * 2 * V) + (RES ? 32 * V : 0);
+    const uint16_t* base = RES ? p.res : p.x;
+    const uint16_t* next = base + uint64_t(r) * uint32_t(RES ? p.ldr : p.ldx) + 8 * at.first;
     if (whole && r < rows) {
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        ptx::cp_async_16_hint(s + 32 * j, x_next + 8 * j * at.step, first);
-        ptx::cp_async_16_hint(s + 32 * (V + j), res_next + 8 * j * at.step, first);
-      }
+      for (int j = 0; j < V; ++j) ptx::cp_async_16_hint(s + 32 * j, next + 8 * j * at.step, first);
     } else {
 #pragma unroll
       for (int j = 0; j < V; ++j) {                  // nothing read beyond the tensor: zeros
         const bool in = r < rows && at(j) < nv;
-        const uint32_t n = in ? 16u : 0u;
-        ptx::cp_async_16_zfill_hint(s + 32 * j, in ? x_next + 8 * j * at.step : p.x, n, first);
-        ptx::cp_async_16_zfill_hint(s + 32 * (V + j), in ? res_next + 8 * j * at.step : p.res, n,
+        ptx::cp_async_16_zfill_hint(s + 32 * j, in ? next + 8 * j * at.step : base, in ? 16u : 0u,
                                     first);
       }
     }
     ptx::cp_async_commit();
   };
+  constexpr std::false_type kO{};
+  constexpr std::true_type kRes{};
 #pragma unroll
-  for (int k = 0; k < kAhead; ++k) prefetch(r_first + k * row_step, k);   // (beyond rows: zeros)
+  for (int k = 0; k < kAhead; ++k) {                 // (beyond rows: zeros)
+    prefetch(r_first + k * row_step, k, kO);
+    prefetch(r_first + k * row_step, k, kRes);
+  }
   // a token's gate: 0 on padding rows
   const auto token = [&](uint32_t r) {
     return r >= rows ? 0.0f : b.token_gate == nullptr ? 1.0f : __ldg(b.token_gate + r);
@@ -184,7 +189,7 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
     const float t = next_t;
     next_t = token(r + row_step);
     float2 x[V][4];                                  // o, then h, then y
-    ptx::cp_async_wait<kAhead - 1>();
+    ptx::cp_async_wait<2 * kAhead - 1>();
     const uint4* s = slot + buf * (32 * 2 * V);
     float2 q = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -193,6 +198,7 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
 #pragma unroll
       for (int k = 0; k < 4; ++k) q = __ffma2_rn(x[j][k], x[j][k], q);
     }
+    prefetch(r + kAhead * row_step, buf, kO);
     float f = t;
     if (post) {
       const float sum = row_sum(q.x + q.y, red, phase, warps, lane, grp, tpr);
@@ -206,6 +212,7 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
     // ---- the stream; a gate of 0 leaves it as it is, whatever o holds
     const float2 f2 = make_float2(f, f);
     q = make_float2(0.0f, 0.0f);
+    ptx::cp_async_wait<2 * kAhead - 1>();
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       uint4 h = s[32 * (V + j)];
@@ -226,7 +233,7 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
 #pragma unroll
       for (int k = 0; k < 4; ++k) q = __ffma2_rn(x[j][k], x[j][k], q);
     }
-    prefetch(r + kAhead * row_step, buf);
+    prefetch(r + kAhead * row_step, buf, kRes);
     buf = buf + 1 == kAhead ? 0 : buf + 1;
 
     const float sum = row_sum(q.x + q.y, red, phase, warps, lane, grp, tpr);
@@ -276,10 +283,10 @@ cudaError_t launch_branch(const NormParams& n, const BranchParams& more, int* ct
   BranchParams b = more;
   b.n = n;
   // Two vectors a thread up to 4096 columns, four beyond: us with two / four
-  //   1 x 4096, row copy                     4.1 /  6.4
-  //   8192 x 4096, row copy                 41.2 / 42.6     with checkpoints 54.4 / 56.0
-  //   8192 x 4096, both copies              57.0 / 55.8     with checkpoints 70.3 / 68.8
-  //   8192 x 5120, both, with checkpoints  103.7 / 86.0
+  //   1 x 4096, row copy                     4.0 /  6.5
+  //   8192 x 4096, row copy                 40.5 / 42.7     with checkpoints 53.0 / 54.9
+  //   8192 x 4096, both copies              56.2 / 56.0     with checkpoints 69.9 / 69.3
+  //   8192 x 5120, both, with checkpoints  103.7 / 86.0     (at an earlier state of the kernel)
   // A row's sums, and so its last bits, must not depend on how many rows there are: the rule goes
   // by the columns alone.
   const RowPlan pl = row_plan(n.cols, n.cols <= 4096 ? 2 : 4, n.cols <= 4096 ? 256 : 384);

@@ -12,12 +12,13 @@
 // rounding to bf16 is the output's alone.
 //
 // 8192 x 4096 from both checkpoints, with dres, moves 338 MB: 61.4 us (49.8 at a copy's rate), of
-// which branch_sums_kernel about 3; from bf16 403 MB in 67.0 (59.4). What bounds it: 16 warps an SM,
-// by registers, for rows that are chains of two sums; 36 instructions an element from checkpoints
-// (29 from bf16). A CTA of three groups with four vectors and 168 registers a thread took 121. Wide
-// rows have one group an SM and nothing beside it: 4096 x 8192 66.5 us, 8192 x 5120 105 (62), 2048 x
-// 16384 (clusters of two) 117, 1024 x 32768 (of four) 207; with four vectors a thread in one CTA
-// the last two took 182 and more.
+// which branch_sums_kernel about 3; from bf16 403 MB in 67.0 (59.4). What bounds it: 16 warps an
+// SM, by registers, for rows that are chains of two sums; 36 instructions an element from
+// checkpoints (29 from bf16). A CTA of three groups with four vectors and 168 registers a thread
+// took 121; dy and h copied apart from dres and o, each refilled as soon as read, 67. Wide rows have
+// one group an SM and nothing beside it: 4096 x 8192 66.5 us, 8192 x 5120 105 (62), 2048 x 16384
+// (clusters of two) 117, 1024 x 32768 (of four) 207; with four vectors a thread in one CTA the last
+// two took 182 and more.
 #include <algorithm>
 #include <type_traits>
 
@@ -76,9 +77,9 @@ __host__ __device__ constexpr int bwd_row_bytes() {      // of a thread
 // whole vectors: they are applied to a vector's sums and to its other factors, not to its elements
 // (69.7 us -> 65.1 with dy, h and o kept in registers), and whole warps run a form of the row's
 // step in which nothing is tested (-> 61.4).
-// CL: a row of more than 8192 columns, whose two column sums a thread no longer fit in the registers
-// of one CTA, lies in the two or four CTAs of a cluster, each of which adds the others' parts of the
-// row's sums, which arrive in shared memory.
+// CL: a row of more than 8192 columns, whose two column sums a thread no longer fit in the
+// registers of one CTA, lies in the two or four CTAs of a cluster, each of which adds the others'
+// parts of the row's sums, which arrive in shared memory.
 template <int V, bool HCK, bool OCK, int CL>
 __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ BranchBwdParams p) {
   constexpr int kBufs = kBwdBufs;
@@ -353,6 +354,7 @@ __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ Branc
   if (p.part != nullptr) {
     // the groups' sums, added by the first group in order, by way of the slots (96 V nt bytes or
     // more where there are several groups, of which 64 V nt are used)
+    static_assert(kBwdBufs * bwd_row_bytes<V, HCK, OCK>() >= 64 * V, "the slots hold both sums");
     float4* sums = reinterpret_cast<float4*>(slots);
     const int n = 2 * V * nt;
     if (rpc > 1) {
