@@ -119,14 +119,6 @@ __device__ __forceinline__ float max8_abs(const float2 (&y)[4]) {
   return max3_abs(max3_abs(m, y[2].y, y[3].x), y[3].y, 0.0f);
 }
 
-// q += the squares of eight packed bf16 values, two an instruction.
-__device__ __forceinline__ void add_squares8(uint4 v, float2& q) {
-  float2 f[4];
-  widen8(v, f);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) q = __ffma2_rn(f[k], f[k], q);
-}
-
 // The sum of a row's threads (a group of tpr: 16, or a whole number of warps), the same in each of
 // them: over the lanes, then over the warps in order. One barrier of the group's own; red's two
 // halves are used by turns, so the next sum need not wait for the last reader of this one.
