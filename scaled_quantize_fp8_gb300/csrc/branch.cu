@@ -199,6 +199,9 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
       for (int k = 0; k < 4; ++k) q = __ffma2_rn(x[j][k], x[j][k], q);
     }
     prefetch(r + kAhead * row_step, buf, kO);
+    // (the checkpoints before the sums' barriers: 2048 x 16384 73.3 us, behind them 77.1)
+    if (b.o_codes != nullptr)
+      ckpt_row<V, FULL>(x, b.o_codes + elem, b.o_scale + sc, lane, at, nv, live, first);
     float f = t;
     if (post) {
       const float sum = row_sum(q.x + q.y, red, phase, warps, lane, grp, tpr);
@@ -206,8 +209,6 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
       if (live && lane == 0 && b.rstd_o != nullptr) b.rstd_o[r] = ro;
       f = ro * t;
     }
-    if (b.o_codes != nullptr)
-      ckpt_row<V, FULL>(x, b.o_codes + elem, b.o_scale + sc, lane, at, nv, live, first);
 
     // ---- the stream; a gate of 0 leaves it as it is, whatever o holds
     const float2 f2 = make_float2(f, f);
@@ -236,11 +237,11 @@ __global__ void __maxnreg__(V <= 4 ? 80 : 128)
     prefetch(r + kAhead * row_step, buf, kRes);
     buf = buf + 1 == kAhead ? 0 : buf + 1;
 
+    if (b.h_codes != nullptr)
+      ckpt_row<V, FULL>(x, b.h_codes + elem, b.h_scale + sc, lane, at, nv, live, first);
     const float sum = row_sum(q.x + q.y, red, phase, warps, lane, grp, tpr);
     const float rstd = rsqrtf(fmaf(sum, p.inv_cols, p.eps));
     if (live && lane == 0 && p.rstd != nullptr) p.rstd[r] = rstd;
-    if (b.h_codes != nullptr)
-      ckpt_row<V, FULL>(x, b.h_codes + elem, b.h_scale + sc, lane, at, nv, live, first);
     if (!want_y) return;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
