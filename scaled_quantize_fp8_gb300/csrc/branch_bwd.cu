@@ -11,14 +11,14 @@
 // go to the workspace and branch_sums_kernel adds them in a fixed order. dh goes on in fp32: its
 // rounding to bf16 is the output's alone.
 //
-// 8192 x 4096 from both checkpoints, with dres, moves 338 MB: 61.4 us (49.8 at a copy's rate), of
+// 8192 x 4096 from both checkpoints, with dres, moves 338 MB: 60.8 us (49.8 at a copy's rate), of
 // which branch_sums_kernel about 3; from bf16 403 MB in 67.0 (59.4). What bounds it: 16 warps an
 // SM, by registers, for rows that are chains of two sums; 36 instructions an element from
 // checkpoints (29 from bf16). A CTA of three groups with four vectors and 168 registers a thread
-// took 121; dy and h copied apart from dres and o, each refilled as soon as read, 67. Wide rows have
-// one group an SM and nothing beside it: 4096 x 8192 66.5 us, 8192 x 5120 105 (62), 2048 x 16384
-// (clusters of two) 117, 1024 x 32768 (of four) 207; with four vectors a thread in one CTA the last
-// two took 182 and more.
+// took 121; dy and h copied apart from dres and o, each refilled as soon as read, 67; gamma in shared
+// memory 61.7. Wide rows have one group an SM and nothing beside it: 4096 x 8192 65.7 us, 8192 x
+// 5120 103 (62), 2048 x 16384 (clusters of two) 116, 1024 x 32768 (of four) 202; with four vectors
+// a thread in one CTA the last two took 182 and more.
 #include <algorithm>
 #include <type_traits>
 
@@ -273,6 +273,9 @@ __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ Branc
       }
       c = fmaf(c2.x + c2.y, f, c);
     }
+    uint4 er[V];                                    // read before the barrier (61.4 -> 60.8)
+#pragma unroll
+    for (int j = 0; j < V; ++j) er[j] = dres ? s[32 * (V + j)] : make_uint4(0, 0, 0, 0);
     c = -p.inv_cols * sum_of(c);
 
     // ---- dh, s, S
@@ -281,12 +284,7 @@ __global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ Branc
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float2 w[4], e[4], (&xj)[4] = x[j], (&gj)[4] = g[j];
-      if (dres) {
-        widen8(s[32 * (V + j)], e);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) e[k] = make_float2(0.0f, 0.0f);
-      }
+      widen8(er[j], e);
       const float fc = hf[HCK ? j : 0] * c;
       const float2 fc2 = make_float2(fc, fc);
 #pragma unroll
