@@ -388,3 +388,83 @@ def test_nothing_written_outside(kind, rows, cols):
     torch.cuda.synchronize()
     for big, n in held:
         assert bool((big[:guard] == 0x5A).all()) and bool((big[guard + n:] == 0x5A).all())
+
+
+# ---------------------------------------------------------------------------- surroundings
+
+def _fields(q):
+    return [t for t in (q.row, q.col, q.row_scale, q.col_scale, q.amax, q.scale) if t is not None]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows,cols", [(3, 256), (200, 1152)])
+def test_one_copy_alone(kind, rows, cols):
+    """The column copy without the row copy, and the other way round: the same bytes as with both."""
+    rec = F.Recipe(kind=kind)
+    o, res = (to_dev_bf16(bf16_bits_normal(rows, cols, seed=s)) for s in (1, 2))
+    g = _dev_gamma(_gamma(cols), False)
+
+    def run(**kw):
+        return F.branch_rmsnorm_quantize(rec, o, res, g, gamma_post=g, **kw)[0]
+
+    both, row, col = run(), run(want_col=False), run(want_row=False)
+    torch.cuda.synchronize()
+    assert row.col is None and col.row is None
+    assert torch.equal(both.row, row.row) and torch.equal(both.col, col.col)
+    if both.amax is not None:
+        assert torch.equal(both.amax, row.amax) and torch.equal(both.amax, col.amax)
+
+
+def test_streams_graphs_and_calls_side_by_side():
+    """The calls run on the given stream with buffers from its pool, two of them at once, and can be
+    captured; the bytes are those of calls in turn."""
+    rec, rows, cols = F.Recipe(kind="delayed"), 700, 2064
+    o, res = (to_dev_bf16(bf16_bits_normal(rows, cols, seed=s)) for s in (1, 2))
+    g, t = _dev_gamma(_gamma(cols), False), torch.rand(rows, device="cuda")
+
+    def step(stream=None):
+        cks = [F.empty_checkpoint(rows, cols) for _ in range(2)]
+        q, h, rstd, ro, _ = F.branch_rmsnorm_quantize(
+            rec, o, res, g, gamma_post=g, token_gate=t, branch_ckpt=cks[0], h_ckpt=cks[1],
+            stream=stream)
+        back = F.checkpoint_read(F.checkpoint(h, stream=stream), stream=stream)
+        again = F.checkpoint_quantize(rec, cks[1], rstd, g, stream=stream)
+        return [*_fields(q), h, rstd, ro, back, *_fields(again), cks[0].codes, cks[0].scale,
+                cks[1].codes, cks[1].scale]
+
+    ref = step()
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    got = [step(s) for s in sides]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for _ in range(2):
+        for x in captured:
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+    for other in (*got, captured):
+        assert all(torch.equal(a, b) for a, b in zip(ref, other))
+
+
+def test_refused_calls_leave_no_error_behind():
+    """What the library refuses is not launched, and the next call runs."""
+    x = to_dev_bf16(bf16_bits_normal(4, 256, seed=1))
+    g, rec = torch.ones(256, device="cuda"), F.Recipe(kind="mxfp8")
+    ck = F.empty_checkpoint(4, 256)
+    for bad in (dict(scale=float("nan")), dict(eps_post=-1.0), dict(branch_ckpt=ck, h_ckpt=ck)):
+        with pytest.raises(F._lib.Fp8Error):
+            F.branch_rmsnorm_quantize(rec, x, x, g, **bad)
+    with pytest.raises(ValueError):
+        F.branch_rmsnorm_quantize(rec, x, x, g, gate=g[:128])
+    with pytest.raises(TypeError):
+        F.branch_rmsnorm_quantize(rec, x, x.cpu(), g)
+    with pytest.raises(TypeError):
+        F.checkpoint(x, out=F.empty_checkpoint(4, 256, device="cpu"))
+    with pytest.raises(F._lib.Fp8Error):
+        F.checkpoint(x[:, :200].contiguous())
+    F.branch_rmsnorm_quantize(rec, x, x, g, h_ckpt=ck)
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite(F.checkpoint_read(ck).float()).all())
