@@ -649,6 +649,13 @@ def _one_device(*tensors):
             raise ValueError("the tensors of a call lie on the current device")
 
 
+def _copies(out: QTensor, want_row, want_col):
+    """The buffers of `out` that a call with these copies writes or reads."""
+    row = (out.row, out.row_scale) if want_row else ()
+    col = (out.col, out.col_scale) if want_col else ()
+    return (*row, *col, out.amax, out.scale, out.scale_inv)
+
+
 def _columns(t: Optional[torch.Tensor], cols, name: str):
     """Address and type of an optional bf16 or fp32 vector of [cols]."""
     if t is None:
@@ -797,7 +804,6 @@ def branch_rmsnorm_quantize(recipe: Optional[Recipe], branch: torch.Tensor,
                               post_fp32, gate_fp32, _gamma(gamma, cols), scale,
                               eps if eps_post is None else eps_post, eps)
     rc = out_ref = None
-    on_gpu = True
     if want_row or want_col:
         block = recipe.kind in ("mxfp8", "blockwise")
         q = 128 if block else 16
@@ -806,12 +812,11 @@ def branch_rmsnorm_quantize(recipe: Optional[Recipe], branch: torch.Tensor,
             with torch.cuda.stream(stream):
                 out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
                                     device=branch.device)
-        ct, on_gpu = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
+        ct, _ = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
         fields = recipe._fields()
         out_ref, rc = ctypes.byref(ct), L.pack_recipe(*fields)
+        tensors += _copies(out, want_row, want_col)
     _one_device(*tensors)
-    if not on_gpu:
-        _not_on_gpu()
     args = (rc, inp, want_row, want_col, h.data_ptr(),
             None if rstd_branch is None else rstd_branch.data_ptr(), rstd.data_ptr(),
             None if y is None else y.data_ptr(), o_ck, h_ck, out_ref)
@@ -856,10 +861,8 @@ def checkpoint_quantize(recipe: Recipe, ck: Checkpoint, rstd: Optional[torch.Ten
         with torch.cuda.stream(stream):
             out = empty_qtensor(recipe, padded, cols, "activation", want_row, want_col,
                                 device=ck.codes.device)
-    ct, on_gpu = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
-    _one_device(ck.codes, ck.scale, rstd, gamma, workspace)
-    if not on_gpu:
-        _not_on_gpu()
+    ct, _ = _packed_out(out, recipe, padded, cols, want_row, want_col, block)
+    _one_device(ck.codes, ck.scale, rstd, gamma, workspace, *_copies(out, want_row, want_col))
     fields = recipe._fields()
     rc = L.pack_recipe(*fields)
     args = (rc, c, rows, cols, None if rstd is None else rstd.data_ptr(),

@@ -983,7 +983,9 @@ fp8_status fp8_branch_rmsnorm_bwd(const fp8_branch_grad* in, const fp8_branch_gr
   FP8_TRY(check_ptr(out->dh));
   FP8_TRY(check_ptr(out->dbranch));
   if (out->dh == out->dbranch || same(out->dgamma, out->dgamma_post) ||
-      same(out->dgamma, out->dgate) || same(out->dgamma_post, out->dgate))
+      same(out->dgamma, out->dgate) || same(out->dgamma_post, out->dgate) ||
+      same(out->dtoken_gate, out->dgamma) || same(out->dtoken_gate, out->dgamma_post) ||
+      same(out->dtoken_gate, out->dgate))
     return FP8_ERR_SHAPE;                   // one buffer for two outputs
   for (const void* d : {out->dh, out->dbranch}) {     // in place only where the rows lie alike
     if ((d == in->dy && in->ld_dy != cols) || (d == in->dres && in->ld_dres != cols) ||

@@ -326,3 +326,8 @@ def test_binding_refuses_cpu_tensors():
 def test_a_checkpoint_has_the_shape_of_its_tensor():
     ck = binding.empty_checkpoint(3, 144, device="cpu")
     assert ck.shape == (3, 144) and ck.scale.shape == (3, 8) and ck.device.type == "cpu"
+
+
+def test_one_buffer_for_a_gate_gradient_and_a_sum(lib):
+    for name in ("dgamma", "dgamma_post", "dgate"):
+        assert _bwd(lib, dtoken_gate=0xE800, **{name: 0xE800}) == SHAPE

@@ -468,3 +468,37 @@ def test_refused_calls_leave_no_error_behind():
     F.branch_rmsnorm_quantize(rec, x, x, g, h_ckpt=ck)
     torch.cuda.synchronize()
     assert bool(torch.isfinite(F.checkpoint_read(ck).float()).all())
+
+
+class _Elsewhere(torch.Tensor):
+    """A tensor that says it lies on another device."""
+
+    def get_device(self):
+        return 1
+
+
+def test_tensors_of_another_device_are_refused():
+    """Kernels run on the current device: inputs and outputs that lie on another are refused, the
+    copies' buffers among them."""
+    x = to_dev_bf16(bf16_bits_normal(128, 256, seed=2))
+    g, rstd = torch.ones(256, device="cuda"), torch.ones(128, device="cuda")
+    rec, ck = F.Recipe(kind="mxfp8"), F.checkpoint(x)
+    away = lambda t: t.as_subclass(_Elsewhere)          # noqa: E731
+    outs = []
+    for name in ("row", "col", "row_scale", "col_scale"):
+        out = F.empty_qtensor(rec, 128, 256, "activation")
+        setattr(out, name, away(getattr(out, name)))
+        outs.append(out)
+    delayed = F.empty_qtensor(F.Recipe(kind="delayed"), 128, 256, "activation")
+    delayed.amax = away(delayed.amax)
+    calls = [lambda o=o: F.branch_rmsnorm_quantize(rec, x, x, g, out=o) for o in outs]
+    calls += [lambda o=o: F.checkpoint_quantize(rec, ck, out=o) for o in outs]
+    calls += [lambda: F.branch_rmsnorm_quantize(F.Recipe(kind="delayed"), x, x, g, out=delayed),
+              lambda: F.branch_rmsnorm_quantize(rec, x, x, away(g)),
+              lambda: F.branch_rmsnorm_bwd(x, x, rstd, g, x, dh=away(torch.empty_like(x))),
+              lambda: F.branch_rmsnorm_bwd(x, F.Checkpoint(ck.codes, away(ck.scale)), rstd, g, x),
+              lambda: F.rmsnorm_bwd(x, F.Checkpoint(away(ck.codes), ck.scale), rstd, g),
+              lambda: F.checkpoint(away(x)), lambda: F.checkpoint_read(ck, out=away(x))]
+    for call in calls:
+        with pytest.raises(ValueError, match="current device"):
+            call()
