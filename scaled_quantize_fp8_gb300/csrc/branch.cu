@@ -11,7 +11,7 @@
 // backward pass reads. The column copy is made by the norm's column kernel from h, in L2.
 //
 // 8192 x 4096 with both MXFP8 copies and both checkpoints has to move 340 MB, 50.0 us at the 6791
-// GB/s of a copy; the two kernels take 69.7, the row kernel alone (305 MB, 44.9) 52.9, 0.85 of that
+// GB/s of a copy; the two kernels take 68.7, the row kernel alone (305 MB, 44.9) 52.5, 0.86 of that
 // rate. What bounds it: the row kernel's time does not follow its instructions (28 to 41 an
 // element, all within 3 us); half of its stalls are for shuffles and shared memory, its warps (24
 // an SM, by registers) go through two sums of a row with a barrier each. The column kernel adds 17
@@ -287,7 +287,8 @@ cudaError_t launch_branch(const NormParams& n, const BranchParams& more, int* ct
   //   1 x 4096, row copy                     4.0 /  6.5
   //   8192 x 4096, row copy                 40.5 / 42.7     with checkpoints 53.0 / 54.9
   //   8192 x 4096, both copies              56.2 / 56.0     with checkpoints 69.9 / 69.3
-  //   8192 x 5120, both, with checkpoints  103.7 / 86.0     (at an earlier state of the kernel)
+  //   8192 x 5120, both, with checkpoints  103.7 / 86.0
+  // (before the checkpoints came in front of the sums' barriers, which took up to 4 us off).
   // A row's sums, and so its last bits, must not depend on how many rows there are: the rule goes
   // by the columns alone.
   const RowPlan pl = row_plan(n.cols, n.cols <= 4096 ? 2 : 4, n.cols <= 4096 ? 256 : 384);
