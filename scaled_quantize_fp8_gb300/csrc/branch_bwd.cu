@@ -16,9 +16,11 @@
 // SM, by registers, for rows that are chains of two sums; 36 instructions an element from
 // checkpoints (29 from bf16). A CTA of three groups with four vectors and 168 registers a thread
 // took 121; dy and h copied apart from dres and o, each refilled as soon as read, 67; gamma in shared
-// memory 61.7. Wide rows have one group an SM and nothing beside it: 4096 x 8192 65.7 us, 8192 x
-// 5120 103 (62), 2048 x 16384 (clusters of two) 116, 1024 x 32768 (of four) 202; with four vectors
-// a thread in one CTA the last two took 182 and more.
+// memory 61.7; one exchange a row, of its second sum and the next row's first, for which dy and h
+// are widened twice and three rows lie in shared memory, 66.0. Wide rows have one group an SM and
+// nothing beside it: 4096 x 8192 65.7 us, 8192 x 5120 91 (62), 2048 x 16384 (clusters of two) 116,
+// 1024 x 32768 (of four) 202; with four vectors a thread in one CTA the last two took 182 and more,
+// with one exchange a row 95 and 181.
 #include <algorithm>
 #include <type_traits>
 
@@ -80,10 +82,11 @@ __host__ __device__ constexpr int bwd_row_bytes() {      // of a thread
 // CL: a row of more than 8192 columns, whose two column sums a thread no longer fit in the
 // registers of one CTA, lies in the two or four CTAs of a cluster, each of which adds the others'
 // parts of the row's sums, which arrive in shared memory.
-template <int V, bool HCK, bool OCK, int CL>
-__global__ void __maxnreg__(128) branch_bwd_kernel(const __grid_constant__ BranchBwdParams p) {
+// REGS: registers a thread, 128, or 96 for CTAs of more than 512 threads.
+template <int V, bool HCK, bool OCK, int CL, int REGS>
+__global__ void __maxnreg__(REGS) branch_bwd_kernel(const __grid_constant__ BranchBwdParams p) {
   constexpr int kBufs = kBwdBufs;
-  __shared__ alignas(16) float red[2][16];
+  __shared__ alignas(16) float red[2][REGS < 128 ? 32 : 16];     // (20 words for 20 warps: 93 us, not 91)
   __shared__ float other[2][CL];
   extern __shared__ uint4 slots[];
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
@@ -478,12 +481,22 @@ struct BranchBwdPlan {
 // One CTA of up to 512 threads per SM, as in the norm's backward pass: its row groups' column sums
 // meet in shared memory, so there are at most as many partials as SMs. Few rows: one vector a
 // thread, and fewer rows a CTA while there are SMs without any.
+// Rows of 577 to 640 vectors, of which two vectors a thread would make one group of ten warps and
+// nothing beside it, have twenty with one vector at 96 registers. From checkpoints / bf16, us, with
+// two and with one: 8192 x 5120 103 and 91 / 93.8 and 89.8, 8192 x 5104 111 and 94, 300 x 5120 13.0
+// and 11.5; 8192 x 4608 101 and 104 / 91 and 99, 8192 x 6144 (at 80 registers) 96.7 and 110. Two
+// groups of ten warps with two vectors, at 96 registers, spill: 120 / 89.8.
 BranchBwdPlan branch_bwd_plan(int64_t rows, int64_t cols) {
   BranchBwdPlan b;
   const int sms = num_sms(), nv = int(cols / 8);
   b.cluster = cols > 16384 ? 4 : cols > 8192 ? 2 : 1;
   const int mine = b.cluster > 1 ? bwd_share(nv, b.cluster) : nv;
-  b.row = row_plan(8 * mine, rows <= 4 * sms ? 1 : 2, 512);
+  if (b.cluster == 1 && nv > 576 && nv <= 640) {
+    const int tpr = (nv + 31) / 32 * 32;
+    b.row = {1, tpr, tpr};
+  } else {
+    b.row = row_plan(8 * mine, rows <= 4 * sms ? 1 : 2, 512);
+  }
   int rpc = b.row.block / b.row.tpr;
   while (rpc > 1 && (rpc / 2) * b.row.tpr >= 128 && rows <= int64_t(rpc / 2) * sms) rpc /= 2;
   b.row.block = rpc * b.row.tpr;
@@ -491,9 +504,9 @@ BranchBwdPlan branch_bwd_plan(int64_t rows, int64_t cols) {
   return b;
 }
 
-template <int V, bool HCK, bool OCK, int CL>
+template <int V, bool HCK, bool OCK, int CL, int REGS>
 cudaError_t launch_bwd(const BranchBwdParams& p, const BranchBwdPlan& b, cudaStream_t st) {
-  auto kern = branch_bwd_kernel<V, HCK, OCK, CL>;
+  auto kern = branch_bwd_kernel<V, HCK, OCK, CL, REGS>;
   const size_t smem = size_t(kBwdBufs) * bwd_row_bytes<V, HCK, OCK>() * std::max(b.row.block, 32) +
                       size_t(V) * 32 * std::max(b.row.tpr, 32);
   if (smem > 47 * 1024) {                                  // 48 KB with the static part
@@ -513,9 +526,11 @@ cudaError_t launch_bwd(const BranchBwdParams& p, const BranchBwdPlan& b, cudaStr
 }
 template <bool HCK, bool OCK>
 cudaError_t launch_bwd(const BranchBwdParams& p, const BranchBwdPlan& b, cudaStream_t st) {
-  if (b.cluster == 4) return launch_bwd<2, HCK, OCK, 4>(p, b, st);
-  if (b.cluster == 2) return launch_bwd<2, HCK, OCK, 2>(p, b, st);
-  return b.row.v == 1 ? launch_bwd<1, HCK, OCK, 1>(p, b, st) : launch_bwd<2, HCK, OCK, 1>(p, b, st);
+  if (b.cluster == 4) return launch_bwd<2, HCK, OCK, 4, 128>(p, b, st);
+  if (b.cluster == 2) return launch_bwd<2, HCK, OCK, 2, 128>(p, b, st);
+  if (b.row.tpr > 512) return launch_bwd<1, HCK, OCK, 1, 96>(p, b, st);
+  return b.row.v == 1 ? launch_bwd<1, HCK, OCK, 1, 128>(p, b, st)
+                      : launch_bwd<2, HCK, OCK, 1, 128>(p, b, st);
 }
 
 }  // namespace

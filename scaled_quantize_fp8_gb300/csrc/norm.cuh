@@ -122,7 +122,8 @@ __device__ __forceinline__ float max8_abs(const float2 (&y)[4]) {
 // The sum of a row's threads (a group of tpr: 16, or a whole number of warps), the same in each of
 // them: over the lanes, then over the warps in order. One barrier of the group's own; red's two
 // halves are used by turns, so the next sum need not wait for the last reader of this one.
-__device__ __forceinline__ float row_sum(float v, float (&red)[2][16], int& phase, int warps,
+template <int N>
+__device__ __forceinline__ float row_sum(float v, float (&red)[2][N], int& phase, int warps,
                                          int lane, int grp, int tpr) {
   if (warps != 0) v += __shfl_xor_sync(0xffffffffu, v, 16);
 #pragma unroll

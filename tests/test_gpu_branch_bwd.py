@@ -145,6 +145,15 @@ def test_many_rows(rows, cols, ckpt):
     check(case(rows, cols, ckpt=ckpt, token=True))
 
 
+@pytest.mark.parametrize("rows,cols", [(1, 4624), (170, 4864), (700, 5104), (2, 5120), (400, 5120),
+                                       (200, 5136)])
+@pytest.mark.parametrize("ckpt", [(True, True), (False, False), (True, False), (False, True)])
+def test_widths_around_5120(rows, cols, ckpt):
+    """Groups of more than 512 threads (4624 to 5120 columns), whole and ragged, and the next width."""
+    check(case(rows, cols, ckpt=ckpt, token=True))
+    check(case(rows, cols, post=False, ckpt=ckpt, dres=False))
+
+
 def test_against_differences():
     """dbranch, dh and dtoken_gate along directions against central differences of the formulas."""
     rows, cols = 24, 512
