@@ -617,7 +617,8 @@ size_t fp8_branch_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  *   dgamma_post = scale * gate * S,  dgate = scale * gamma_post * S,  dtoken_gate[r] = s[r]
  * dbranch and the sums follow from dh before its rounding to bf16. A token whose gate is 0 has a
  * dbranch of zeros and adds nothing to S, whatever its row of branch holds; its dtoken_gate is s,
- * of that row.
+ * of that row. Where the forward pass left rstd or rstd_branch 0 (squares beyond fp32's range), the
+ * row's finite elements count as xh or xo of 0, however large they are.
  *   dh, dbranch   each may be one of dy, dres, h and branch itself when that is contiguous (not
  *                 both the same).
  *   workspace     fp8_branch_rmsnorm_bwd_workspace_bytes() of device scratch.

@@ -75,10 +75,11 @@ __host__ __device__ constexpr int bwd_row_bytes() {      // of a thread
 // tpr threads per row (16, or whole warps), V vectors of eight columns a thread, laid out as in
 // branch_row_kernel. Every thread copies its own elements of the next row to its own slots of
 // shared memory while it works on the present one, whose three steps, mean(a xh), dh and s, and do,
-// it makes in the same registers. rstd and rstd_o, and a checkpoint's powers of two, are factors of
-// whole vectors: they are applied to a vector's sums and to its other factors, not to its elements
+// it makes in the same registers. rstd or rstd_o times a checkpoint's power of two is a factor of
+// whole vectors: it is applied to a vector's sums and to its other factors, not to its elements
 // (69.7 us -> 65.1 with dy, h and o kept in registers), and whole warps run a form of the row's
-// step in which nothing is tested (-> 61.4).
+// step in which nothing is tested (-> 61.4). From bf16 the elements are scaled (see there), within
+// 1 % of the time without at most widths, 3 % at 4112 columns.
 // CL: a row of more than 8192 columns, whose two column sums a thread no longer fit in the
 // registers of one CTA, lies in the two or four CTAs of a cluster, each of which adds the others'
 // parts of the row's sums, which arrive in shared memory.
@@ -242,9 +243,11 @@ __global__ void __maxnreg__(REGS) branch_bwd_kernel(const __grid_constant__ Bran
       if (HCK) hf[HCK ? j : 0] = ckpt_factor(next_he[j]) * rs;
       if (OCK) of[OCK ? j : 0] = ckpt_factor(next_oe[j]) * ro;
     }
-    if (!HCK) hf[0] = rs;
-    if (!OCK) of[0] = ro;
-    // what h and o hold, without those factors: they are applied to sums and to other factors
+    if (!HCK) hf[0] = 1.0f;
+    if (!OCK) of[0] = 1.0f;
+    // what h and o hold. A code's factors are applied to sums and to other factors; bf16 is made xh
+    // and xo where it is read, for a row whose squares overflow has an rstd of 0 and elements
+    // whose products with a gradient may be infinite.
     const auto h_of = [&](int j, float2 (&x)[4]) {
       if constexpr (HCK) ckpt_widen8(q[32 * j], x);
       else widen8(s[32 * (2 * V + j)], x);
@@ -258,6 +261,7 @@ __global__ void __maxnreg__(REGS) branch_bwd_kernel(const __grid_constant__ Bran
     scalars(full_tag, r + step);
 
     // ---- mean(a xh), dgamma
+    const float2 r2 = make_float2(rs, rs), ro2 = make_float2(ro, ro);
     float2 d[V][4], x[V][4];                        // dy, then dh, then u; h, then o
     float c = 0.0f;
 #pragma unroll
@@ -270,6 +274,7 @@ __global__ void __maxnreg__(REGS) branch_bwd_kernel(const __grid_constant__ Bran
       float2 c2 = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        if (!HCK) xj[k] = __fmul2_rn(xj[k], r2);
         const float2 v = __fmul2_rn(d[j][k], xj[k]);
         acc_g[j][k] = __ffma2_rn(v, f2, acc_g[j][k]);
         c2 = __ffma2_rn(v, gj[k], c2);
@@ -282,7 +287,6 @@ __global__ void __maxnreg__(REGS) branch_bwd_kernel(const __grid_constant__ Bran
     c = -p.inv_cols * sum_of(c);
 
     // ---- dh, s, S
-    const float2 r2 = make_float2(rs, rs);
     float s1 = 0.0f;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -304,6 +308,7 @@ __global__ void __maxnreg__(REGS) branch_bwd_kernel(const __grid_constant__ Bran
       float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
+        if (!OCK) xj[k] = __fmul2_rn(xj[k], ro2);
         const float2 v = __fmul2_rn(d[j][k], xj[k]);
         // a gate of 0: whatever o holds, nothing of it reaches the sums
         if (t != 0.0f) acc_s[j][k] = __ffma2_rn(v, ft2, acc_s[j][k]);
