@@ -530,7 +530,7 @@ typedef struct {
  *   dev_status, the shapes, the padding and the refusals: as for fp8_rmsnorm_quantize.
  *   h_bf16        [rows][cols] bf16, contiguous: the new stream. May be in->branch or in->residual
  *                 itself when that is contiguous.
- *   rstd_branch   [rows] fp32 for the backward pass, or NULL (not written without gamma_post).
+ *   rstd_branch   [rows] fp32 for the backward pass, or NULL (not looked at without gamma_post).
  *   rstd          [rows] fp32 or NULL.
  *   branch_ckpt, h_ckpt: checkpoints of branch and of h, written in the same pass; or NULL.
  * A row's results do not depend on the other rows nor on their number (per-tensor scales aside).
@@ -584,9 +584,10 @@ typedef struct {
   const void *gamma_post, *gate;        /* as in the forward pass */
   const float *token_gate;
   const void *gamma;
-  const float *rstd_branch;  /* [rows], with gamma_post: as the forward pass wrote them */
+  const float *rstd_branch;  /* [rows], with gamma_post (else not looked at): as the forward pass
+                                wrote them */
   const float *rstd;         /* [rows] */
-  int64_t ld_dy, ld_dres, ld_h, ld_branch;
+  int64_t ld_dy, ld_dres, ld_h, ld_branch;   /* not looked at without the tensor */
   int64_t rows, cols;
   int32_t gamma_post_fp32, gate_fp32, gamma_fp32;
   float scale;

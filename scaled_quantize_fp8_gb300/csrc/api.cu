@@ -751,6 +751,12 @@ fp8_status check_rows(const void* p, int64_t ld, int64_t cols) {
   return check_pitch(ld, cols);
 }
 
+// The same for the branch's kernels.
+fp8_status check_branch_rows(const void* p, int64_t ld, int64_t cols) {
+  FP8_TRY(check_rows(p, ld, cols));
+  return ld > kBranchMaxRows ? FP8_ERR_SHAPE : FP8_OK;
+}
+
 fp8_status check_floats(const float* p) {
   return reinterpret_cast<uintptr_t>(p) % 4 != 0 ? FP8_ERR_ALIGN : FP8_OK;
 }
@@ -910,11 +916,12 @@ fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe* recipe, const fp8_branc
   FP8_TRY(check_vector(in->gate, in->gate_fp32));
   if (!(in->eps_post >= 0.0f) || !finite(in->eps_post) || !finite(in->scale))
     return FP8_ERR_UNSUPPORTED;
-  if (a.rows > kBranchMaxRows || a.ldx > kBranchMaxRows || a.ldr > kBranchMaxRows)
-    return FP8_ERR_SHAPE;
+  if (a.rows > kBranchMaxRows) return FP8_ERR_SHAPE;
+  if (in->gamma_post == nullptr) rstd_branch = nullptr;      // not written, not looked at
   const bool empty = a.rows == 0 || a.cols == 0;
   if (!empty) {
     if (a.res == nullptr) return FP8_ERR_NULL;
+    if (a.ldx > kBranchMaxRows || a.ldr > kBranchMaxRows) return FP8_ERR_SHAPE;
     if (reinterpret_cast<uintptr_t>(in->token_gate) % 4 != 0 ||
         reinterpret_cast<uintptr_t>(rstd_branch) % 4 != 0)
       return FP8_ERR_ALIGN;
@@ -966,19 +973,18 @@ fp8_status fp8_branch_rmsnorm_bwd(const fp8_branch_grad* in, const fp8_branch_gr
     return FP8_OK;
   }
   if (rows > kBranchMaxRows) return FP8_ERR_SHAPE;
-  for (const int64_t ld : {in->ld_dy, in->ld_dres, in->ld_h, in->ld_branch})
-    if (ld > kBranchMaxRows) return FP8_ERR_SHAPE;
-  FP8_TRY(check_rows(in->dy, in->ld_dy, cols));
-  if (in->dres != nullptr) FP8_TRY(check_rows(in->dres, in->ld_dres, cols));
+  // (what the call does not read does not refuse it)
+  FP8_TRY(check_branch_rows(in->dy, in->ld_dy, cols));
+  if (in->dres != nullptr) FP8_TRY(check_branch_rows(in->dres, in->ld_dres, cols));
   const bool h_ckpt = in->h_ckpt.codes != nullptr, branch_ckpt = in->branch_ckpt.codes != nullptr;
-  FP8_TRY(h_ckpt ? check_checkpoint(&in->h_ckpt) : check_rows(in->h, in->ld_h, cols));
+  FP8_TRY(h_ckpt ? check_checkpoint(&in->h_ckpt) : check_branch_rows(in->h, in->ld_h, cols));
   FP8_TRY(branch_ckpt ? check_checkpoint(&in->branch_ckpt)
-                      : check_rows(in->branch, in->ld_branch, cols));
+                      : check_branch_rows(in->branch, in->ld_branch, cols));
   FP8_TRY(check_ptr(in->gamma));
   if (in->rstd == nullptr || (in->gamma_post != nullptr && in->rstd_branch == nullptr))
     return FP8_ERR_NULL;
   FP8_TRY(check_floats(in->rstd));
-  FP8_TRY(check_floats(in->rstd_branch));
+  if (in->gamma_post != nullptr) FP8_TRY(check_floats(in->rstd_branch));
   FP8_TRY(check_floats(in->token_gate));
   FP8_TRY(check_ptr(out->dh));
   FP8_TRY(check_ptr(out->dbranch));
