@@ -624,7 +624,8 @@ size_t fp8_branch_rmsnorm_bwd_workspace_bytes(int64_t rows, int64_t cols);
  *                 both the same).
  *   workspace     fp8_branch_rmsnorm_bwd_workspace_bytes() of device scratch.
  * Equal calls give equal bits (a fixed order of additions, which follows from the numbers of rows
- * and columns). rows >= 0; cols a multiple of 16, at most 32768. dev_status is not written.
+ * and columns). rows >= 0; cols a multiple of 16, at most 32768; without columns nothing is written.
+ * dev_status is not written.
  */
 fp8_status fp8_branch_rmsnorm_bwd(const fp8_branch_grad *in, const fp8_branch_grad_out *out,
                                   void *workspace, size_t ws_bytes, int32_t *dev_status,

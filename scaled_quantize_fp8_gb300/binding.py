@@ -991,6 +991,9 @@ def branch_rmsnorm_bwd(dy: torch.Tensor, h: "torch.Tensor | Checkpoint", rstd: t
         st = lib.fp8_branch_rmsnorm_bwd(*args, *_buffer(workspace), *rest)
     if st:
         L.check(st, "fp8_branch_rmsnorm_bwd")
+    if cols == 0 and token_gate is not None:     # the library writes nothing: sums of nothing
+        with torch.cuda.stream(stream):
+            out.dtoken_gate.zero_()
     return out
 
 

@@ -65,3 +65,15 @@ def test_forward_and_backward_of_such_rows():
     for t in d[:5]:
         assert bool(torch.isfinite(t.float()).all())
     assert torch.equal(d.dh[6], dres[6]) and not d.dbranch[3].any()
+
+
+def test_no_columns():
+    """A gradient per token is a sum over no columns: zeros, not what the buffer held."""
+    x, t = torch.empty((5, 0), dtype=torch.bfloat16, device="cuda"), torch.ones(5, device="cuda")
+    none, held = torch.empty(0, device="cuda"), torch.full((5,), 7.0, device="cuda")
+    for stream in (None, torch.cuda.Stream()):
+        mine = held.clone()
+        torch.cuda.synchronize()
+        d = F.branch_rmsnorm_bwd(x, x, t, none, x, token_gate=t, dtoken_gate=mine, stream=stream)
+        torch.cuda.synchronize()
+        assert not d.dtoken_gate.any() and d.dh.shape == (5, 0) and d.dgamma.numel() == 0
