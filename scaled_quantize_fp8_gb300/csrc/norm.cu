@@ -64,7 +64,7 @@ __global__ void __maxnreg__(V <= 2 ? 72 : V == 4 ? 80 : 128)
   __shared__ uint32_t redm[16];
   extern __shared__ uint4 slots[];                  // each thread's next rows
   const int tpr = blockDim.x, lane = threadIdx.x, grp = threadIdx.y, rpc = blockDim.y;
-  const int warp = (grp * tpr + lane) >> 5, wl = (grp * tpr + lane) & 31, nv = p.cols >> 3;
+  const int nv = p.cols >> 3;
   const int warps = tpr >> 5;                       // warps per row (0: two rows a warp)
   const bool want_y = OUT != N_STATS || p.y != nullptr || p.part != nullptr;
   // x and the residual are read once; h (x without a residual) is read again by the column kernel,
