@@ -554,6 +554,8 @@ fp8_status fp8_branch_rmsnorm_quantize(const fp8_recipe *recipe, const fp8_branc
  *   y = (h * rstd) * gamma       the norm's output, from the stream's checkpoint and the forward
  *                                pass's rstd; or y = h with rstd and gamma both NULL
  * with h the checkpoint's values: a copy made from them is that of the 8-bit h, not of the bf16 one.
+ * (rstd meets a block's power of two first, which changes nothing but where their product lies below
+ * 2^-126: blocks of magnitudes below 2^-117 / rstd, whose y may be off by more than its roundings.)
  *   in        checkpoint of [rows][cols]
  *   rstd      [rows] fp32, gamma [cols] (gamma_fp32 0: bf16, 1: fp32): both or neither
  *   recipe, want_row, want_col, out, workspace (fp8_rmsnorm_workspace_bytes), shapes and padding:
@@ -567,8 +569,9 @@ fp8_status fp8_checkpoint_quantize(const fp8_recipe *recipe, const fp8_checkpoin
                                    size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
 
 /* fp8_rmsnorm_bwd_checkpoint — fp8_rmsnorm_bwd with h read from its checkpoint (in->h and in->ld_h
- * are not looked at): half of h's memory and a seventh of the call's traffic less. Workspace as for
- * fp8_rmsnorm_bwd. A block whose byte is 0xFF makes its row of dh and its columns of dgamma NaN. */
+ * are not looked at): half of h's memory, and of the call's traffic an eighth less with dres (7 1/32
+ * bytes an element instead of 8), a sixth without (5 1/32 of 6). Workspace as for fp8_rmsnorm_bwd. A
+ * block whose byte is 0xFF makes its row of dh and its columns of dgamma NaN. */
 fp8_status fp8_rmsnorm_bwd_checkpoint(const fp8_norm_grad *in, const fp8_checkpoint *h_ckpt,
                                       void *dh_bf16, float *dgamma, void *workspace,
                                       size_t ws_bytes, int32_t *dev_status, cudaStream_t stream);
