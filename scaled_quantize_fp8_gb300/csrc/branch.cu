@@ -284,11 +284,13 @@ cudaError_t launch_branch(const NormParams& n, const BranchParams& more, int* ct
   BranchParams b = more;
   b.n = n;
   // Two vectors a thread up to 4096 columns, four beyond: us with two / four
-  //   1 x 4096, row copy                     4.0 /  6.5
-  //   8192 x 4096, row copy                 40.5 / 42.7     with checkpoints 53.0 / 54.9
-  //   8192 x 4096, both copies              56.2 / 56.0     with checkpoints 69.9 / 69.3
-  //   8192 x 5120, both, with checkpoints  103.7 / 86.0
-  // (before the checkpoints came in front of the sums' barriers, which took up to 4 us off).
+  //   1 x 4096, row copy                     4.0 /  6.2
+  //   8192 x 4096, row copy                 39.8 / 42.1     with checkpoints 52.5 / 54.2
+  //   8192 x 4096, both copies              55.3 / 54.6     with checkpoints 69.0 / 66.7
+  //   8192 x 2048, both, with checkpoints   36.2 / 38.2
+  //   8192 x 4608, both, with checkpoints   90.9 / 91.5
+  //   8192 x 5120, both, with checkpoints   95.5 / 84.7
+  // (serving and the training step of the examples want the row copy alone).
   // A row's sums, and so its last bits, must not depend on how many rows there are: the rule goes
   // by the columns alone.
   const RowPlan pl = row_plan(n.cols, n.cols <= 4096 ? 2 : 4, n.cols <= 4096 ? 256 : 384);

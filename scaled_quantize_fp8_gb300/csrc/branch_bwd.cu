@@ -12,9 +12,9 @@
 // rounding to bf16 is the output's alone.
 //
 // 8192 x 4096 from both checkpoints, with dres, moves 338 MB: 60.8 us (49.8 at a copy's rate), of
-// which branch_sums_kernel about 3; from bf16 403 MB in 67.0 (59.4). What bounds it: 16 warps an
+// which branch_sums_kernel about 3; from bf16 403 MB in 66.6 (59.4). What bounds it: 16 warps an
 // SM, by registers, for rows that are chains of two sums; 36 instructions an element from
-// checkpoints (29 from bf16). A CTA of three groups with four vectors and 168 registers a thread
+// checkpoints (29.5 from bf16). A CTA of three groups with four vectors and 168 registers a thread
 // took 121; dy and h copied apart from dres and o, each refilled as soon as read, 67; gamma in shared
 // memory 61.7; one exchange a row, of its second sum and the next row's first, for which dy and h
 // are widened twice and three rows lie in shared memory, 66.0. Wide rows have one group an SM and

@@ -9,8 +9,10 @@
 // beyond its end idle.
 //
 // The third is the norm's column kernel with another source, 16.4 us for the MXFP8 column copy of
-// 8192 x 4096 (69 MB: 10.2 at a copy's rate), bound by its instruction slots as that kernel is, and
-// checkpoint_row_kernel for the row copy.
+// 8192 x 4096 (69 MB: 10.2 at a copy's rate), and checkpoint_row_kernel for the row copy, 17.7. No
+// one resource bounds them: DRAM is a quarter busy, of the issue slots 59 and 62 % are used. Their
+// registers allow 25 to 30 % of the warps, too few to cover a chain of load, unpacking, maxima,
+// shuffles and conversion. Both copies (34.1) read and unpack the checkpoint twice.
 #include <algorithm>
 
 #include "ckpt.cuh"
